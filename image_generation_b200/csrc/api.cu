@@ -1,11 +1,13 @@
 // C ABI of libh3dit (declared in include/h3dit.h): argument checks, the
 // workspace plan, TMA tensor-map encoding and the order of kernel launches
 // for one DiT block and one sampling step. All compute runs in the kernels of
-// gemm.cu, gemm_pair.cu, gemm_mx.cu, attention.cu and elementwise.cu; this
-// file only marshals.
+// gemm.cu, gemm_pair.cu, gemm_mx.cu, gemm_fp4.cu, attention.cu, elementwise.cu,
+// gated_norm.cu, rope_axes.cu and fp4.cu; this file only marshals.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <climits>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -32,6 +34,7 @@ constexpr size_t kNoTiled = ~static_cast<size_t>(0);
 
 struct Layout {
   size_t status, resid, xm, qkv, attn, u, mod, cvec, hidden, omod, rope, wptr, bptr;
+  size_t amax;  // fp4_tensor_scale: its counter (kAlign bytes), then the partial maxima
   // MXFP8 precision only
   size_t xq, xq_sf, oq, oq_sf, uq, uq_sf, wq, wq_block;
   MxWeights wq_off;  // offsets inside one block's slice of the wq arena
@@ -80,6 +83,7 @@ Layout plan(const h3dit_config *c) {
   L.rope = take(N * (c->head_dim / 2) * 2 * 4);
   L.wptr = take(static_cast<size_t>(c->n_blocks) * sizeof(void *));
   L.bptr = take(static_cast<size_t>(c->n_blocks) * sizeof(void *));
+  L.amax = take(kAlign + kFp4ScaleParts * sizeof(float));
   if (c->precision == H3DIT_PRECISION_MXFP8) {
     L.xq = take(N * D);
     L.xq_sf = take(mx_sf_bytes(N, D));
@@ -216,6 +220,7 @@ struct h3dit_ctx {
   size_t ws_bytes = 0;
   Layout L{};
   int num_sms = 148;
+  int device = 0;  // current in create
   std::string err;
   // layerwise weight streaming: blocks whose weights are pinned host memory
   std::vector<uint8_t> streamed;  // per block: 1 = weights in host memory
@@ -233,6 +238,8 @@ struct h3dit_ctx {
   std::vector<h3dit_vae_layer_weights> vlayers;
   size_t vpos = 0, vones = 0;  // workspace offsets: position table, a vector of ones
 
+  unsigned *amax_done() { return reinterpret_cast<unsigned *>(ws + L.amax); }
+  float *amax_part() { return reinterpret_cast<float *>(ws + L.amax + kAlign); }
   int *status() { return reinterpret_cast<int *>(ws + L.status); }
   float *resid() { return reinterpret_cast<float *>(ws + L.resid); }
   void *xm() { return ws + L.xm; }
@@ -923,6 +930,7 @@ h3dit_status h3dit_create(const h3dit_config *cfg, const h3dit_time_weights *tim
     delete ctx;
     return H3DIT_ERR_CUDA;
   }
+  ctx->device = dev;
   // where each block's weights live: all on the device, or all in pinned
   // host memory (streamed layer by layer through staging slots)
   ctx->streamed.assign(cfg->n_blocks, 0);
@@ -959,6 +967,7 @@ h3dit_status h3dit_create(const h3dit_config *cfg, const h3dit_time_weights *tim
     bp[l] = blocks[l].b_ada;
   }
   cudaError_t e = cudaMemsetAsync(ctx->status(), 0, sizeof(int), s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(ctx->amax_done(), 0, sizeof(unsigned), s);
   if (e == cudaSuccess)
     e = cudaMemcpyAsync(ctx->ws + L.wptr, wp.data(), wp.size() * sizeof(void *),
                         cudaMemcpyHostToDevice, s);
@@ -1535,8 +1544,10 @@ h3dit_status h3dit_vae_create(const h3dit_vae_config *cfg, const h3dit_vae_weigh
     delete ctx;
     return H3DIT_ERR_CUDA;
   }
+  ctx->device = dev;
   std::vector<float> ones(cfg->width, 1.0f);
   cudaError_t e = cudaMemsetAsync(ctx->status(), 0, sizeof(int), s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(ctx->amax_done(), 0, sizeof(unsigned), s);
   if (e == cudaSuccess)
     e = launch_vae_pos_table(cfg->tile, cfg->width, reinterpret_cast<float *>(ctx->ws + ctx->vpos),
                              ctx->num_sms, s);
@@ -1703,6 +1714,320 @@ h3dit_status h3dit_attention_mx(h3dit_ctx *ctx, const void *q, const void *k, co
   if (!o_sf) return ctx->fail(H3DIT_ERR_INVALID_ARG, "o_sf is NULL");
   return run_attention(ctx, q, k, v, ld_qkv, o, ctx->inner(), n,
                        static_cast<cudaStream_t>(cuda_stream), o_sf);
+}
+
+// ---- 4-bit matrices, the norms around a branch, rotary axes ----
+namespace {
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// These calls launch on the current device, which has to be the context's.
+h3dit_status check_device(h3dit_ctx *ctx) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return ctx->fail(H3DIT_ERR_CUDA, "no current device");
+  if (dev != ctx->device)
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "the current device is %d, the context's is %d", dev,
+                     ctx->device);
+  return H3DIT_OK;
+}
+
+h3dit_status check_fp4(h3dit_ctx *ctx, int format, int rows, int k) {
+  if (format != H3DIT_FP4_MX && format != H3DIT_FP4_NV)
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "unknown FP4 format %d", format);
+  if (rows < 0 || k <= 0) return ctx->fail(H3DIT_ERR_INVALID_ARG, "bad shape %d x %d", rows, k);
+  if (k % 64)
+    return ctx->fail(H3DIT_ERR_UNSUPPORTED, "an FP4 matrix needs columns in multiples of 64 (%d)", k);
+  return H3DIT_OK;
+}
+
+// A matrix to be read as FP4: its type, stride and address.
+h3dit_status check_fp4_source(h3dit_ctx *ctx, const void *src, int f32, long long ld, int k) {
+  if (f32 != 0 && f32 != 1) return ctx->fail(H3DIT_ERR_INVALID_ARG, "src_fp32 must be 0 or 1");
+  if (ld < k || ld % (f32 ? 4 : 8))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "bad row stride %lld for %d columns", ld, k);
+  if (!src || !aligned16(src)) return ctx->fail(H3DIT_ERR_INVALID_ARG, "NULL or misaligned pointer");
+  return H3DIT_OK;
+}
+
+h3dit_status run_linear_fp4(h3dit_ctx *ctx, int format, int epi, Fp4GemmParams &p, const void *a,
+                            const void *w, cudaStream_t s) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return ctx->fail(H3DIT_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const int kernel_epi = epi == H3DIT_EPI_GELU && p.out_sf ? static_cast<int>(kEpiGeluFp4) : epi;
+  const Fp4GemmPlan plan = fp4_gemm_plan(format, kernel_epi, &p, ctx->num_sms);
+  CUtensorMap ta, tb;
+  // rows of packed bytes, read in boxes of 128 bytes; past the row's end they read 0
+  auto encode = [&](CUtensorMap *t, const void *base, int rows, int box) {
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.k / 2), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.k / 2)};
+    const cuuint32_t boxes[2] = {128, static_cast<cuuint32_t>(box)};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, boxes,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  };
+  CUresult r = encode(&ta, a, p.m, plan.box_a);
+  if (r == CUDA_SUCCESS) r = encode(&tb, w, p.n, plan.box_b);
+  if (r != CUDA_SUCCESS) return ctx->fail(H3DIT_ERR_CUDA, "tensor map encode failed (%d)", (int)r);
+  Launch L(ctx, H3DIT_KERNEL_LINEAR_FP4, s);
+  return ctx->cuda(launch_gemm_fp4(format, kernel_epi, ta, tb, p, plan, s), "FP4 gemm launch");
+}
+
+}  // namespace
+
+size_t h3dit_fp4_scale_bytes(int32_t format, int32_t rows, int32_t k) {
+  if ((format != H3DIT_FP4_MX && format != H3DIT_FP4_NV) || rows <= 0 || k <= 0 || k % 64) return 0;
+  return fp4_sf_bytes(format, rows, k);
+}
+
+h3dit_status h3dit_fp4_tensor_scale(h3dit_ctx *ctx, const void *src, int32_t src_fp32, int64_t ld,
+                                    int32_t rows, int32_t k, float *scale_out, void *cuda_stream) {
+  if (!ctx) return H3DIT_ERR_INVALID_ARG;
+  h3dit_status st = check_fp4(ctx, H3DIT_FP4_NV, rows, k);
+  if (st) return st;
+  if (rows == 0) return H3DIT_OK;
+  if ((st = check_fp4_source(ctx, src, src_fp32, ld, k))) return st;
+  if (!scale_out || !aligned4(scale_out))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "scale_out is NULL or misaligned");
+  if ((st = check_device(ctx))) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  Launch L(ctx, H3DIT_KERNEL_FP4_QUANTIZE, s);
+  return ctx->cuda(launch_fp4_tensor_scale(src, src_fp32 != 0, ld, rows, k, ctx->amax_part(),
+                                           ctx->amax_done(), scale_out, ctx->num_sms, s),
+                   "FP4 tensor scale launch");
+}
+
+h3dit_status h3dit_fp4_quantize(h3dit_ctx *ctx, int32_t format, const void *src, int32_t src_fp32,
+                                int64_t ld, int32_t rows, int32_t k, const float *tensor_scale,
+                                void *codes, void *scales, void *cuda_stream) {
+  if (!ctx) return H3DIT_ERR_INVALID_ARG;
+  h3dit_status st = check_fp4(ctx, format, rows, k);
+  if (st) return st;
+  if (rows == 0) return H3DIT_OK;
+  if ((st = check_fp4_source(ctx, src, src_fp32, ld, k))) return st;
+  if (!codes || !scales || !aligned16(codes) || !aligned16(scales) || !aligned4(tensor_scale))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "NULL or misaligned pointer");
+  if (format == H3DIT_FP4_MX && tensor_scale)
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "MXFP4 is quantized without a tensor scale");
+  if ((st = check_device(ctx))) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  Launch L(ctx, H3DIT_KERNEL_FP4_QUANTIZE, s);
+  return ctx->cuda(launch_fp4_quantize(format, src, src_fp32 != 0, ld, rows, k, tensor_scale,
+                                       static_cast<uint8_t *>(codes),
+                                       static_cast<uint8_t *>(scales), ctx->num_sms, s),
+                   "FP4 quantize launch");
+}
+
+h3dit_status h3dit_fp4_dequantize(h3dit_ctx *ctx, int32_t format, const void *codes,
+                                  const void *scales, const float *tensor_scale, int32_t rows,
+                                  int32_t k, void *out, void *cuda_stream) {
+  if (!ctx) return H3DIT_ERR_INVALID_ARG;
+  h3dit_status st = check_fp4(ctx, format, rows, k);
+  if (st) return st;
+  if (rows == 0) return H3DIT_OK;
+  if (!codes || !scales || !out || !aligned16(codes) || !aligned16(scales) || !aligned16(out) ||
+      !aligned4(tensor_scale))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "NULL or misaligned pointer");
+  if ((st = check_device(ctx))) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  Launch L(ctx, H3DIT_KERNEL_FP4_QUANTIZE, s);
+  return ctx->cuda(launch_fp4_dequantize(format, static_cast<const uint8_t *>(codes),
+                                         static_cast<const uint8_t *>(scales), rows, k,
+                                         tensor_scale, out, ctx->num_sms, s),
+                   "FP4 dequantize launch");
+}
+
+h3dit_status h3dit_linear_fp4(h3dit_ctx *ctx, int32_t format, int32_t epilogue, const void *a,
+                              const void *a_sf, const float *a_scale, const void *w,
+                              const void *w_sf, const float *w_scale, int32_t m, int32_t n,
+                              int32_t k, void *out, void *out_sf, const float *out_scale,
+                              const float *bias, const float *gate, const float *resid,
+                              void *cuda_stream) {
+  if (!ctx) return H3DIT_ERR_INVALID_ARG;
+  h3dit_status st = check_fp4(ctx, format, m, k);
+  if (st) return st;
+  if (epilogue != H3DIT_EPI_STORE && epilogue != H3DIT_EPI_GELU &&
+      epilogue != H3DIT_EPI_GATED_RESIDUAL)
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "epilogue %d is not offered on FP4 operands", epilogue);
+  if (n <= 0) return ctx->fail(H3DIT_ERR_INVALID_ARG, "bad shape %d x %d x %d", m, n, k);
+  if (out_sf && epilogue != H3DIT_EPI_GELU)
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "only GELU writes FP4 (out_sf)");
+  if (n % (out_sf ? 64 : 32))
+    return ctx->fail(H3DIT_ERR_UNSUPPORTED, "FP4 linear: n = %d is not a multiple of %d", n,
+                     out_sf ? 64 : 32);
+  if (m == 0) return H3DIT_OK;
+  if ((static_cast<long long>(m) + 127) / 128 * ((static_cast<long long>(n) + 63) / 64) > INT_MAX)
+    return ctx->fail(H3DIT_ERR_UNSUPPORTED, "FP4 linear: %d x %d is too large", m, n);
+  for (const void *ptr : {a, a_sf, w, w_sf, static_cast<const void *>(out)})
+    if (!ptr || !aligned16(ptr))
+      return ctx->fail(H3DIT_ERR_INVALID_ARG, "FP4 linear: NULL or misaligned pointer");
+  if (!aligned16(out_sf) || !aligned16(bias) || !aligned4(a_scale) || !aligned4(w_scale) ||
+      !aligned4(out_scale))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "FP4 linear: misaligned pointer");
+  if (epilogue == H3DIT_EPI_GATED_RESIDUAL && (!gate || !aligned16(gate) || !aligned16(resid)))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "gated residual needs a 16-byte aligned gate and resid");
+  if (epilogue != H3DIT_EPI_GATED_RESIDUAL && (gate || resid))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "gate and resid belong to GATED_RESIDUAL");
+  if (out_scale && (!out_sf || format != H3DIT_FP4_NV))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "out_scale belongs to an NVFP4 output");
+  if ((st = check_device(ctx))) return st;
+  Fp4GemmParams p{};
+  p.m = m;
+  p.n = n;
+  p.k = k;
+  p.a_sf = static_cast<const uint8_t *>(a_sf);
+  p.b_sf = static_cast<const uint8_t *>(w_sf);
+  p.a_scale = a_scale;
+  p.b_scale = w_scale;
+  p.bias = bias;
+  p.gate = gate;
+  p.resid = resid ? resid : static_cast<const float *>(out);
+  p.out = out;
+  p.out_sf = static_cast<uint8_t *>(out_sf);
+  p.out_scale = out_scale;
+  p.gelu_tanh = ctx->cfg.gelu_tanh;
+  p.status = ctx->status();
+  return run_linear_fp4(ctx, format, epilogue, p, a, w, static_cast<cudaStream_t>(cuda_stream));
+}
+
+h3dit_status h3dit_gated_norm(h3dit_ctx *ctx, const h3dit_norm_args *g, void *cuda_stream) {
+  if (!ctx) return H3DIT_ERR_INVALID_ARG;
+  if (!g) return ctx->fail(H3DIT_ERR_INVALID_ARG, "args is NULL");
+  const int D = ctx->cfg.hidden;
+  if (g->rows < 0 || g->rows_per_group < 0)
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "negative row count");
+  if (g->out_kind < H3DIT_NORM_OUT_BF16 || g->out_kind > H3DIT_NORM_OUT_FP4_NV)
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "unknown output kind %d", g->out_kind);
+  if (g->out_kind == H3DIT_NORM_OUT_MXFP8 && D % 128)
+    return ctx->fail(H3DIT_ERR_UNSUPPORTED, "MXFP8 needs hidden %% 128 == 0");
+  if ((g->branch_fp32 != 0 && g->branch_fp32 != 1) || (g->post_norm != 0 && g->post_norm != 1))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "branch_fp32 and post_norm are 0 or 1");
+  if (g->rows == 0) return H3DIT_OK;
+  if (!g->x || !g->out) return ctx->fail(H3DIT_ERR_INVALID_ARG, "x or out is NULL");
+  for (const void *ptr :
+       {static_cast<const void *>(g->x), static_cast<const void *>(g->x_out), g->branch,
+        static_cast<const void *>(g->post_weight), static_cast<const void *>(g->pre_weight),
+        static_cast<const void *>(g->gate), static_cast<const void *>(g->shift),
+        static_cast<const void *>(g->scale), static_cast<const void *>(g->out),
+        static_cast<const void *>(g->out_sf)})
+    if (!aligned16(ptr)) return ctx->fail(H3DIT_ERR_INVALID_ARG, "misaligned pointer");
+  if (!aligned4(g->out_scale)) return ctx->fail(H3DIT_ERR_INVALID_ARG, "misaligned out_scale");
+  if (!g->branch && (g->post_norm || g->gate))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "post_norm and gate need a branch");
+  if (g->post_weight && !g->post_norm)
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "post_weight needs post_norm");
+  if ((g->out_kind == H3DIT_NORM_OUT_BF16) != (g->out_sf == nullptr))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "out_sf goes with the MXFP8 and FP4 outputs");
+  if (g->out_scale && g->out_kind != H3DIT_NORM_OUT_FP4_NV)
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "out_scale belongs to an NVFP4 output");
+  const bool groups = g->rows_per_group > 0 && g->rows_per_group < g->rows;
+  if (groups && (g->gate || g->shift || g->scale) && (g->ld_mod < D || g->ld_mod % 4))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "bad modulation stride %lld",
+                     static_cast<long long>(g->ld_mod));
+  h3dit_status st = check_device(ctx);
+  if (st) return st;
+  GatedNormParams p{};
+  p.x = g->x;
+  p.x_out = g->x_out;
+  p.branch = g->branch;
+  p.gate = g->gate;
+  p.shift = g->shift;
+  p.scale = g->scale;
+  p.post_weight = g->post_weight;
+  p.pre_weight = g->pre_weight;
+  p.out = g->out;
+  p.out_sf = static_cast<uint8_t *>(g->out_sf);
+  p.out_scale = g->out_scale;
+  p.ld_mod = groups ? g->ld_mod : 0;
+  p.n = g->rows;
+  p.d = D;
+  p.rows_per_group = groups ? g->rows_per_group : g->rows;
+  p.eps = ctx->cfg.norm_eps;
+  p.residual_scale = g->residual_scale;
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  Launch L(ctx, H3DIT_KERNEL_GATED_NORM, s);
+  return ctx->cuda(launch_gated_norm(p, g->branch_fp32 != 0, g->post_norm != 0, g->out_kind,
+                                     ctx->num_sms, s),
+                   "gated norm launch");
+}
+
+h3dit_status h3dit_rope_axes(h3dit_ctx *ctx, const h3dit_rope_spec *spec, const float *positions,
+                             int32_t n, int32_t io_fp32, const void *q, int64_t ld_q, void *q_out,
+                             int64_t ld_q_out, int32_t heads_q, const void *k, int64_t ld_k,
+                             void *k_out, int64_t ld_k_out, int32_t heads_k,
+                             const float *q_weight, const float *k_weight, int32_t flags,
+                             void *cuda_stream) {
+  if (!ctx) return H3DIT_ERR_INVALID_ARG;
+  if (!spec) return ctx->fail(H3DIT_ERR_INVALID_ARG, "spec is NULL");
+  const int dh = spec->head_dim;
+  if (dh < 16 || dh > 2 * kRopeMaxPairs || dh % 16)
+    return ctx->fail(H3DIT_ERR_UNSUPPORTED, "head_dim %d is not a multiple of 16 up to %d", dh,
+                     2 * kRopeMaxPairs);
+  long long pairs = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (spec->sections[i] < 0) return ctx->fail(H3DIT_ERR_INVALID_ARG, "negative section");
+    pairs += spec->sections[i];
+  }
+  if (2 * pairs > dh)
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "%lld pairs do not fit into head_dim %d", pairs, dh);
+  if (!(spec->theta > 0.f) || !(spec->theta < INFINITY))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "theta must be positive and finite");
+  if ((spec->interleaved != 0 && spec->interleaved != 1) || (io_fp32 != 0 && io_fp32 != 1) ||
+      (flags & ~H3DIT_ROPE_INVERSE))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "unknown flag");
+  if (n < 0 || heads_q < 0 || heads_k < 0 || heads_q > (1 << 20) || heads_k > (1 << 20))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "bad token or head count");
+  if ((flags & H3DIT_ROPE_INVERSE) && (q_weight || k_weight))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "the inverse turns back; it undoes no norm");
+  if (n == 0 || (heads_q == 0 && heads_k == 0)) return H3DIT_OK;
+  RopeAxesParams p{};
+  const struct {
+    const void *src;
+    void *dst;
+    int64_t ld, ld_out;
+    int heads;
+    const float *weight;
+  } part[2] = {{q, q_out, ld_q, ld_q_out, heads_q, q_weight},
+               {k, k_out, ld_k, ld_k_out, heads_k, k_weight}};
+  for (int w = 0; w < 2; ++w) {
+    if (part[w].heads == 0) continue;
+    const long long width = static_cast<long long>(part[w].heads) * dh;
+    const int unit = io_fp32 ? 4 : 8;
+    if (!part[w].src || !part[w].dst || !aligned16(part[w].src) || !aligned16(part[w].dst) ||
+        !aligned16(part[w].weight))
+      return ctx->fail(H3DIT_ERR_INVALID_ARG, "rope: NULL or misaligned pointer");
+    if (part[w].ld < width || part[w].ld_out < width || part[w].ld % unit || part[w].ld_out % unit)
+      return ctx->fail(H3DIT_ERR_INVALID_ARG, "rope: bad row stride");
+    if (part[w].src == part[w].dst && part[w].ld != part[w].ld_out)
+      return ctx->fail(H3DIT_ERR_INVALID_ARG, "rope in place needs one row stride");
+    p.src[w] = part[w].src;
+    p.dst[w] = part[w].dst;
+    p.ld_src[w] = part[w].ld;
+    p.ld_dst[w] = part[w].ld_out;
+    p.heads[w] = part[w].heads;
+    p.weight[w] = part[w].weight;
+  }
+  if (!positions || !aligned4(positions))
+    return ctx->fail(H3DIT_ERR_INVALID_ARG, "positions is NULL or misaligned");
+  h3dit_status st = check_device(ctx);
+  if (st) return st;
+  p.pos = positions;
+  p.n = n;
+  p.head_dim = dh;
+  p.inverse = flags & H3DIT_ROPE_INVERSE;
+  p.norm = q_weight || k_weight;
+  p.eps = ctx->cfg.norm_eps;
+  const double log_theta = std::log(static_cast<double>(spec->theta));
+  int at = 0;
+  for (int i = 0; i < 3; ++i) {
+    p.sec[i] = spec->sections[i];
+    for (int j = 0; j < p.sec[i]; ++j)
+      p.half_turns[at++] = std::exp(-log_theta * j / p.sec[i]) / 3.14159265358979323846;
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  Launch L(ctx, H3DIT_KERNEL_ROPE_AXES, s);
+  return ctx->cuda(launch_rope_axes(p, io_fp32 != 0, spec->interleaved != 0, ctx->num_sms, s),
+                   "rope axes launch");
 }
 
 h3dit_status h3dit_time_embed_static(const float *w_t1, const float *b_t1, const float *w_t2,

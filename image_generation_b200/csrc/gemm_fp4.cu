@@ -1,0 +1,370 @@
+// Block-scaled FP4 tcgen05 GEMM: acc[m, n] = sum_k A[m, k] W[n, k] with A and W
+// in E2M1 (two per byte) and a scale per 32 (MXFP4, E8M0) or per 16 (NVFP4,
+// E4M3) consecutive k of every row, fp32 accumulate in tensor memory; then
+// alpha = (A's tensor scale) (W's tensor scale), the bias, and one of
+//   STORE            out bf16 = v
+//   GELU             out bf16 = GELU(v), or the same rounded to FP4
+//   GATED_RESIDUAL   out fp32 = resid + gate * v
+// with v = alpha acc + bias.
+//
+// Structure (one CTA per SM, persistent over 128 x 128 output tiles):
+//   warp 0      TMA producer: A and W boxes of 128 rows x 128 bytes (256 k, in
+//               128-byte swizzle) and that k-block's scale blocks into a ring;
+//   warp 1      MMA issuer: tcgen05.cp of the scale blocks into tensor memory,
+//               then one MMA (M128 N128 K64) per 64 k;
+//   warps 2..5  epilogue: one row of the tile per thread.
+// k is a multiple of 64: a last k-block with fewer than four groups of 64 reads
+// zeros past the row (TMA fill) and issues only the MMAs whose k exist, so the
+// padding of the scale blocks is never multiplied.
+#include "fp4.cuh"
+#include "gemm_epilogue.cuh"
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace h3 {
+namespace {
+
+using namespace gemm_detail;
+
+constexpr int BM = 128;
+constexpr int BKB = 128;       // bytes of a row per k-block
+constexpr int BK = 2 * BKB;    // elements
+constexpr int SF = 512;        // bytes of a scale block: 128 rows x 4 scales
+constexpr uint32_t TMEM_COLS = 512;
+
+template <int FMT>
+struct Kb {  // scale blocks per k-block, and MMAs that share one
+  static constexpr int CHUNKS = BK / (4 * Fp4<FMT>::BLOCK);
+  static constexpr int PER_CHUNK = 4 / CHUNKS;
+};
+
+// alpha = ga * gw, as a factor and a second one that is 1 unless the product
+// leaves the normal range of fp32.
+struct Alpha {
+  float a, b;
+};
+H3_DEV Alpha tensor_alpha(const float *ga, const float *gw) {
+  const float x = ga ? __ldg(ga) : 1.f, y = gw ? __ldg(gw) : 1.f;
+  const float p = x * y;
+  if (fabsf(p) >= 1.17549435e-38f && fabsf(p) < INFINITY) return {p, 1.f};
+  return {x, y};
+}
+
+// v = alpha acc + bias for 32 columns, then the epilogue, straight to memory.
+template <int FMT, int EPI>
+H3_DEV void finish32(const Fp4GemmParams &p, const Alpha &al, float (&v)[32], int row, int col) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] *= al.a;
+  if (al.b != 1.f) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] *= al.b;
+  }
+  if (p.bias) {
+    const float4 *b = reinterpret_cast<const float4 *>(p.bias + col);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const float4 bb = __ldg(b + q);
+      v[4 * q + 0] += bb.x;
+      v[4 * q + 1] += bb.y;
+      v[4 * q + 2] += bb.z;
+      v[4 * q + 3] += bb.w;
+    }
+  }
+  const size_t at = static_cast<size_t>(row) * p.n + col;
+  if constexpr (EPI == kEpiGatedResidual) {
+    const float4 *g = reinterpret_cast<const float4 *>(p.gate + col);
+    const float4 *x = reinterpret_cast<const float4 *>(p.resid + at);
+    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      float4 a = x[q];
+      const float4 gg = __ldg(g + q);
+      a.x = fmaf(gg.x, v[4 * q + 0], a.x);
+      a.y = fmaf(gg.y, v[4 * q + 1], a.y);
+      a.z = fmaf(gg.z, v[4 * q + 2], a.z);
+      a.w = fmaf(gg.w, v[4 * q + 3], a.w);
+      o[q] = a;
+    }
+  } else {
+    if constexpr (EPI != kEpiStore) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = gelu_f(v[i], p.gelu_tanh);
+    }
+    if constexpr (EPI == kEpiGeluFp4) {
+      const Fp4Tensor t = fp4_tensor(FMT == kFp4Nv ? p.out_scale : nullptr);
+      uint32_t q[4], sb[2];
+      fp4_quant32<FMT>(v, t, q, sb);
+      st_global_v4(static_cast<uint8_t *>(p.out) + at / 2, q[0], q[1], q[2], q[3]);
+      const int chunks = (p.n / Fp4<FMT>::BLOCK + 3) / 4;
+      const size_t o = mx_sf_offset(row, col / Fp4<FMT>::BLOCK, chunks);
+      if constexpr (FMT == kFp4Nv) {
+        *reinterpret_cast<uint16_t *>(p.out_sf + o) = static_cast<uint16_t>(sb[0] | (sb[1] << 8));
+      } else {
+        p.out_sf[o] = static_cast<uint8_t>(sb[0]);
+        // a row that ends with two of its last four scales: the others are 0
+        if (col + 32 == p.n && p.n % 128 == 64)
+          *reinterpret_cast<uint16_t *>(p.out_sf + o + 1) = 0;
+      }
+    } else {
+      store_bf16_row<32>(static_cast<uint16_t *>(p.out) + at, v);
+    }
+  }
+}
+
+// ------------------------------------------------------------ one CTA per tile
+namespace one {
+constexpr int BN = 128;
+constexpr int THREADS = 192;
+constexpr int STAGES = 4;
+constexpr int A_BYTES = BM * BKB, B_BYTES = BN * BKB;
+
+template <int FMT>
+struct Tile {
+  static constexpr int SF_BYTES = Kb<FMT>::CHUNKS * SF;  // of A or W, one k-block
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 2 * SF_BYTES;
+  static constexpr int NUM_BARS = 2 * STAGES + 4 + 1;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + NUM_BARS * 8 + 16;
+  static constexpr uint32_t SF_COL0 = 2 * BN;
+  static constexpr uint32_t SF_COLS = 8 * Kb<FMT>::CHUNKS;  // per stage: A, then W
+};
+static_assert(Tile<kFp4Nv>::SF_COL0 + STAGES * Tile<kFp4Nv>::SF_COLS <= TMEM_COLS, "TMEM budget");
+static_assert(Tile<kFp4Nv>::STAGE_BYTES % 1024 == 0 && Tile<kFp4Mx>::STAGE_BYTES % 1024 == 0,
+              "stages start on swizzle atoms");
+
+template <int FMT, int EPI>
+__global__ void __launch_bounds__(THREADS, 1)
+    gemm_fp4(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
+             const Fp4GemmParams p) {
+  using T = Tile<FMT>;
+  constexpr bool NV = FMT == kFp4Nv;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * T::STAGE_BYTES);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + T::NUM_BARS);
+
+  __shared__ int aborted;
+  if (grid_aborted(p.status, &aborted)) return;
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = smem_u32(bars);
+  auto FULL = [&](int s) { return bar0 + 8u * s; };
+  auto EMPTY = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto TFULL = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+  auto TEMPTY = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
+  const uint32_t DRAIN = bar0 + 8u * (2 * STAGES + 4);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(FULL(s), 1);
+      mbar_init(EMPTY(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(TFULL(a), 1);
+      mbar_init(TEMPTY(a), 128);
+    }
+    mbar_init(DRAIN, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tma_a);
+    tma_prefetch_desc(&tma_b);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int num_tiles = p.tiles_m * p.tiles_n;
+  const int kblocks = (p.k + BK - 1) / BK;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      long long issued = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+        int tm, tn;
+        tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait(EMPTY(stage), phase ^ 1, p.status)) {
+            ok = false;
+            break;
+          }
+          const int c0 = kb * Kb<FMT>::CHUNKS;
+          const uint32_t sf_bytes = min(Kb<FMT>::CHUNKS, p.chunks - c0) * SF;
+          // a box counts whole, also where it reads past the matrix
+          mbar_arrive_expect_tx(FULL(stage), A_BYTES + B_BYTES + 2 * sf_bytes);
+          const uint32_t sa = sbase + stage * T::STAGE_BYTES;
+          tma_load_2d(sa, &tma_a, kb * BKB, tm * BM, FULL(stage));
+          tma_load_2d(sa + A_BYTES, &tma_b, kb * BKB, tn * BN, FULL(stage));
+          bulk_load(sa + A_BYTES + B_BYTES,
+                    p.a_sf + (static_cast<size_t>(tm) * p.chunks + c0) * SF, sf_bytes, FULL(stage));
+          bulk_load(sa + A_BYTES + B_BYTES + T::SF_BYTES,
+                    p.b_sf + (static_cast<size_t>(tn) * p.chunks + c0) * SF, sf_bytes, FULL(stage));
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      for (int i = 0; i < STAGES && i < issued; ++i) {
+        if (--stage < 0) {
+          stage = STAGES - 1;
+          phase ^= 1;
+        }
+        mbar_wait(FULL(stage), phase, p.status, false);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+        if (!mbar_wait(TEMPTY(acc), acc_phase ^ 1, p.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait(FULL(stage), phase, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = sbase + stage * T::STAGE_BYTES;
+          const uint32_t sb = sa + A_BYTES;
+          const uint32_t sfa = tmem + T::SF_COL0 + T::SF_COLS * stage;
+          const uint32_t sfb = sfa + 4 * Kb<FMT>::CHUNKS;
+          const int groups = min(4, (p.k - kb * BK) / 64);
+#pragma unroll
+          for (int c = 0; c < Kb<FMT>::CHUNKS; ++c) {
+            if (c * Kb<FMT>::PER_CHUNK >= groups) break;
+            tmem_cp_sf(sfa + 4 * c, desc_sf_copy(sb + B_BYTES + c * SF));
+            tmem_cp_sf(sfb + 4 * c, desc_sf_copy(sb + B_BYTES + T::SF_BYTES + c * SF));
+          }
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            if (g >= groups) break;
+            const int c = g / Kb<FMT>::PER_CHUNK, id = 2 * (g % Kb<FMT>::PER_CHUNK);
+            umma_fp4<NV>(d, desc_sw128(sa + g * 32, 16, 1024), desc_sw128(sb + g * 32, 16, 1024),
+                         idesc_fp4(BM, BN, NV, id), sfa + 4 * c, sfb + 4 * c,
+                         (kb | g) != 0 ? 1u : 0u);
+          }
+          umma_commit(EMPTY(stage));
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        umma_commit(TFULL(acc));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      }
+      umma_commit(DRAIN);
+      mbar_wait(DRAIN, 0, p.status, false);
+    }
+  } else {
+    const int sub = warp & 3;
+    const Alpha al = tensor_alpha(p.a_scale, p.b_scale);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
+      int tm, tn;
+      tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
+      const bool ok = mbar_wait(TFULL(acc), acc_phase, p.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t tbase =
+          tmem + (static_cast<uint32_t>(sub * 32) << 16) + static_cast<uint32_t>(acc * BN);
+      const int row = tm * BM + sub * 32 + lane;
+#pragma unroll 1
+      for (int c = 0; c < BN && tn * BN + c < p.n; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(tbase + c, r);
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+        if (row < p.m) finish32<FMT, EPI>(p, al, v, row, tn * BN + c);
+      }
+      tc_fence_before();
+      mbar_arrive(TEMPTY(acc));
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+template <int FMT, int EPI>
+cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const Fp4GemmParams &p, int grid,
+                   cudaStream_t s) {
+  static PerDevice smem_attr;
+  cudaError_t e = set_smem_once(smem_attr, gemm_fp4<FMT, EPI>, Tile<FMT>::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  gemm_fp4<FMT, EPI><<<grid, THREADS, Tile<FMT>::SMEM_BYTES, s>>>(a, b, p);
+  return cudaGetLastError();
+}
+}  // namespace one
+
+template <int FMT, int EPI>
+cudaError_t launch_epi(const CUtensorMap &a, const CUtensorMap &b, const Fp4GemmParams &p,
+                       const Fp4GemmPlan &plan, cudaStream_t s) {
+  return one::launch<FMT, EPI>(a, b, p, plan.grid, s);
+}
+
+template <int FMT>
+cudaError_t launch_fmt(int epi, const CUtensorMap &a, const CUtensorMap &b, const Fp4GemmParams &p,
+                       const Fp4GemmPlan &plan, cudaStream_t s) {
+  switch (epi) {
+    case kEpiStore:
+      return launch_epi<FMT, kEpiStore>(a, b, p, plan, s);
+    case kEpiGelu:
+      return launch_epi<FMT, kEpiGelu>(a, b, p, plan, s);
+    case kEpiGatedResidual:
+      return launch_epi<FMT, kEpiGatedResidual>(a, b, p, plan, s);
+    case kEpiGeluFp4:
+      return launch_epi<FMT, kEpiGeluFp4>(a, b, p, plan, s);
+    default:
+      return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+Fp4GemmPlan fp4_gemm_plan(int fmt, int epilogue, Fp4GemmParams *p, int num_sms) {
+  (void)epilogue;
+  Fp4GemmPlan plan{};
+  p->chunks = fp4_chunks(fmt, p->k);
+  p->tiles_m = (p->m + BM - 1) / BM;
+  p->tiles_n = (p->n + one::BN - 1) / one::BN;
+  plan.box_a = BM;
+  plan.box_b = one::BN;
+  const long long tiles = static_cast<long long>(p->tiles_m) * p->tiles_n;
+  plan.grid = static_cast<int>(tiles < num_sms ? tiles : num_sms);
+  return plan;
+}
+
+cudaError_t launch_gemm_fp4(int fmt, int epilogue, const CUtensorMap &a, const CUtensorMap &b,
+                            const Fp4GemmParams &p, const Fp4GemmPlan &plan, cudaStream_t s) {
+  return fmt == kFp4Mx ? launch_fmt<kFp4Mx>(epilogue, a, b, p, plan, s)
+                       : launch_fmt<kFp4Nv>(epilogue, a, b, p, plan, s);
+}
+
+}  // namespace h3

@@ -62,6 +62,7 @@ enum Epilogue : int {
   kEpiGelu = 2,
   kEpiGatedResidual = 3,
   kEpiGeluMx = 4,  // GELU, written as MXFP8 (E4M3 + per-32 E8M0 scales)
+  kEpiGeluFp4 = 5,  // GELU, written as FP4 of the operands' format
 };
 
 // MXFP8 scale-factor layout (one E8M0 byte per 32 elements along K) for a
@@ -202,6 +203,89 @@ cudaError_t launch_mx_tile_sf(const uint8_t *sf, int n, int k, uint8_t *tiled, c
 // bf16 [rows, k] (row stride ld elements) -> E4M3 [rows, k] + scales.
 cudaError_t launch_mx_quantize(const void *src, long long ld, int rows, int k, uint8_t *dst,
                                uint8_t *sf, cudaStream_t s);
+
+// FP4 matrices (fp4.cuh has the formats): MXFP4 and NVFP4.
+enum Fp4Format : int { kFp4Mx = 0, kFp4Nv = 1 };
+constexpr int kFp4ScaleParts = 2048;  // partial maxima of the tensor scale (workspace floats)
+inline int fp4_block(int fmt) { return fmt == kFp4Mx ? 32 : 16; }
+// 512-byte scale blocks along a row of k elements, and bytes of the array.
+inline int fp4_chunks(int fmt, int k) { return (k / fp4_block(fmt) + 3) / 4; }
+inline size_t fp4_sf_bytes(int fmt, long long rows, int k) {
+  return static_cast<size_t>((rows + 127) / 128) * static_cast<size_t>(fp4_chunks(fmt, k)) * 512;
+}
+// src bf16 or fp32 [rows, k], row stride ld elements.
+cudaError_t launch_fp4_quantize(int fmt, const void *src, bool f32, long long ld, int rows, int k,
+                                const float *g, uint8_t *dst, uint8_t *sf, int num_sms,
+                                cudaStream_t s);
+cudaError_t launch_fp4_dequantize(int fmt, const uint8_t *q, const uint8_t *sf, int rows, int k,
+                                  const float *g, void *out, int num_sms, cudaStream_t s);
+// part: kFp4ScaleParts floats of scratch; done: a counter that is 0 between calls.
+cudaError_t launch_fp4_tensor_scale(const void *src, bool f32, long long ld, int rows, int k,
+                                    float *part, unsigned *done, float *out, int num_sms,
+                                    cudaStream_t s);
+
+// The product of two FP4 matrices (gemm_fp4.cu).
+struct Fp4GemmParams {
+  int m, n, k;
+  int tiles_m, tiles_n;
+  int chunks;                   // 512-byte scale blocks along k
+  const uint8_t *a_sf, *b_sf;
+  const float *a_scale, *b_scale;  // tensor scales (device scalars), or null for 1
+  const float *bias;            // [n] or null
+  const float *gate;            // gated residual: [n]
+  const float *resid;           // gated residual: [m, n], may be `out`
+  void *out;                    // dense [m, n]
+  uint8_t *out_sf;              // GELU to FP4
+  const float *out_scale;       // GELU to NVFP4: tensor scale of the output, or null for 1
+  int gelu_tanh;
+  int *status;
+};
+// Rows of the A and W boxes and how many CTAs the launch takes.
+struct Fp4GemmPlan {
+  int box_a, box_b, grid;
+  bool pair;
+};
+Fp4GemmPlan fp4_gemm_plan(int fmt, int epilogue, Fp4GemmParams *p, int num_sms);
+cudaError_t launch_gemm_fp4(int fmt, int epilogue, const CUtensorMap &a, const CUtensorMap &b,
+                            const Fp4GemmParams &p, const Fp4GemmPlan &plan, cudaStream_t s);
+
+// x_out = residual_scale x + gate * (post ? RMSNorm(branch) post_weight : branch);
+// out = RMSNorm(x_out) pre_weight (1 + scale) + shift (gated_norm.cu).
+enum NormOut : int { kNormBf16 = 0, kNormMxfp8 = 1, kNormFp4Mx = 2, kNormFp4Nv = 3 };
+struct GatedNormParams {
+  const float *x;
+  float *x_out;               // may be x; null: not written
+  const void *branch;         // bf16 or fp32 [n, d], or null
+  const float *gate, *shift, *scale;  // rows of ld_mod floats, or null for 1, 0, 0
+  const float *post_weight, *pre_weight;  // [d], or null for 1
+  void *out;
+  uint8_t *out_sf;
+  const float *out_scale;     // NVFP4: tensor scale, or null for 1
+  long long ld_mod;
+  int n, d;
+  int rows_per_group;         // rows that share one row of gate, shift and scale
+  float eps, residual_scale;
+};
+cudaError_t launch_gated_norm(const GatedNormParams &p, bool branch_f32, bool post, int out_kind,
+                              int num_sms, cudaStream_t s);
+
+// Optional RMSNorm per head, then the rotation by positions on three axes (rope_axes.cu).
+constexpr int kRopeMaxPairs = 128;
+struct RopeAxesParams {
+  const float *pos;           // [n, 3]
+  const void *src[2];         // q, k rows
+  void *dst[2];
+  long long ld_src[2], ld_dst[2];  // elements
+  const float *weight[2];     // [head_dim] or null
+  int heads[2];
+  int n, head_dim;
+  int sec[3];                 // pairs of each axis
+  int inverse, norm;
+  float eps;
+  double half_turns[kRopeMaxPairs];  // angle per unit of position, over pi
+};
+cudaError_t launch_rope_axes(const RopeAxesParams &p, bool f32, bool interleaved, int num_sms,
+                             cudaStream_t s);
 
 cudaError_t launch_time_embed(float t, float t_scale, const float *w1, const float *b1,
                               const float *w2, const float *b2, float *hidden, float *c_out,

@@ -283,6 +283,38 @@ __host__ __device__ constexpr uint32_t idesc_mxf8(int m, int n, int sf_id) {
          (static_cast<uint32_t>(m >> 4) << 24) | (static_cast<uint32_t>(sf_id) << 29);
 }
 
+// The FP4 products: E2M1 operands (K 64 per instruction), with one E8M0 scale
+// per 32 (kind::mxf4, two scales per row and instruction) or one E4M3 scale per
+// 16 (kind::mxf4nvf4, four).
+template <bool NV>
+H3_DEV void umma_fp4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                     uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  if constexpr (NV)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor of the FP4 kinds: [4,6) B scale id (first scale byte:
+// 0 or 2), [7,10) A format 1 = E2M1, [10,12) B format, [17,23) N >> 3, 23 scale
+// format (0 E4M3, 1 E8M0), [24,29) M >> 4, [29,31) A scale id.
+__host__ __device__ constexpr uint32_t idesc_fp4(int m, int n, bool nv, int sf_id) {
+  return (static_cast<uint32_t>(sf_id) << 4) | (1u << 7) | (1u << 10) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (nv ? 0u : 1u << 23) |
+         (static_cast<uint32_t>(m >> 4) << 24) | (static_cast<uint32_t>(sf_id) << 29);
+}
+
 // MXFP8 (OCP MX) quantization of 32 consecutive values: scale exponent
 // X = floor(log2(amax)) - 8 stored as the E8M0 byte X + 127 (0 for a zero or
 // subnormal block), elements v * 2^-X rounded to E4M3 (nearest even,

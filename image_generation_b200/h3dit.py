@@ -43,8 +43,19 @@ H3DIT_IPC_HANDLE_BYTES = 64
 H3DIT_ATTN_STAMP_SLOTS = 32
 H3DIT_ATTN_STAMP_STEPS = 300
 
+H3DIT_FP4_MX = 0
+H3DIT_FP4_NV = 1
+
+H3DIT_NORM_OUT_BF16 = 0
+H3DIT_NORM_OUT_MXFP8 = 1
+H3DIT_NORM_OUT_FP4_MX = 2
+H3DIT_NORM_OUT_FP4_NV = 3
+
+H3DIT_ROPE_INVERSE = 1
+
 KERNEL_KINDS = ["time_embed", "adaln", "rmsnorm", "qkv", "attention", "out_proj", "ffn1",
-                "ffn2", "rope_table", "pack", "mx_quantize", "io"]
+                "ffn2", "rope_table", "pack", "mx_quantize", "io", "fp4_quantize", "linear_fp4",
+                "gated_norm", "rope_axes"]
 
 
 class h3dit_config(C.Structure):
@@ -70,6 +81,21 @@ class h3dit_block_weights(C.Structure):
 class h3dit_io_weights(C.Structure):
     _fields_ = [("w_in", C.c_void_p), ("b_in", C.c_void_p), ("w_mod", C.c_void_p),
                 ("b_mod", C.c_void_p), ("w_out", C.c_void_p), ("b_out", C.c_void_p)]
+
+
+class h3dit_norm_args(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("x_out", C.c_void_p), ("branch", C.c_void_p),
+                ("branch_fp32", C.c_int32), ("post_norm", C.c_int32),
+                ("post_weight", C.c_void_p), ("pre_weight", C.c_void_p), ("gate", C.c_void_p),
+                ("shift", C.c_void_p), ("scale", C.c_void_p), ("ld_mod", C.c_int64),
+                ("rows", C.c_int32), ("rows_per_group", C.c_int32),
+                ("residual_scale", C.c_float), ("out_kind", C.c_int32), ("out", C.c_void_p),
+                ("out_sf", C.c_void_p), ("out_scale", C.c_void_p)]
+
+
+class h3dit_rope_spec(C.Structure):
+    _fields_ = [("head_dim", C.c_int32), ("sections", C.c_int32 * 3), ("theta", C.c_float),
+                ("interleaved", C.c_int32)]
 
 
 class h3dit_vae_config(C.Structure):
@@ -105,6 +131,7 @@ def _load() -> C.CDLL:
             f"{LIB_PATH} is missing: build it with `python -m image_generation_b200.build`")
     lib = C.CDLL(LIB_PATH)
     p, i32, f32, sz = C.c_void_p, C.c_int32, C.c_float, C.c_size_t
+    i64 = C.c_int64
     sig = {
         "h3dit_status_string": (C.c_char_p, [i32]),
         "h3dit_last_error": (C.c_char_p, [p]),
@@ -128,6 +155,15 @@ def _load() -> C.CDLL:
         "h3dit_block_linear_mx": (i32, [p, i32, i32, p, p, i32, p, p, p, p, p]),
         "h3dit_rmsnorm_modulate_mx": (i32, [p, p, p, p, p, p, i32, p]),
         "h3dit_attention_mx": (i32, [p, p, p, p, i32, p, p, i32, p]),
+        "h3dit_fp4_scale_bytes": (sz, [i32, i32, i32]),
+        "h3dit_fp4_tensor_scale": (i32, [p, p, i32, i64, i32, i32, p, p]),
+        "h3dit_fp4_quantize": (i32, [p, i32, p, i32, i64, i32, i32, p, p, p, p]),
+        "h3dit_fp4_dequantize": (i32, [p, i32, p, p, p, i32, i32, p, p]),
+        "h3dit_linear_fp4": (i32, [p, i32, i32, p, p, p, p, p, p, i32, i32, i32, p, p, p, p, p, p,
+                                   p]),
+        "h3dit_gated_norm": (i32, [p, C.POINTER(h3dit_norm_args), p]),
+        "h3dit_rope_axes": (i32, [p, C.POINTER(h3dit_rope_spec), p, i32, i32, p, i64, p, i64, i32,
+                                  p, i64, p, i64, i32, p, p, i32, p]),
         "h3dit_embed_latent": (i32, [p, p, i32, i32, i32, p, p, p, p]),
         "h3dit_output_modulation": (i32, [p, p, p, p, p, p]),
         "h3dit_output_euler": (i32, [p, p, p, p, p, p, i32, i32, i32, f32, p]),
@@ -210,6 +246,17 @@ def mx_sf_offset(row: int, s: int, k: int) -> int:
     return ((row // 128) * (k // 128) + s // 4) * 512 + (row % 32) * 16 + ((row // 32) % 4) * 4 + s % 4
 
 
+def fp4_scale_bytes(fmt: int, rows: int, k: int) -> int:
+    return int(lib.h3dit_fp4_scale_bytes(fmt, rows, k))
+
+
+def make_rope_spec(head_dim: int, sections: Sequence[int], theta: float = 10000.0,
+                   interleaved: bool = False) -> h3dit_rope_spec:
+    """Rotary axes of one head: sections are the pairs of the frame, row and
+    column axis."""
+    return h3dit_rope_spec(head_dim, (C.c_int32 * 3)(*sections), theta, int(interleaved))
+
+
 def grids_array(grids: Sequence[Tuple[int, int, int]]):
     arr = (h3dit_grid * max(1, len(grids)))()
     for i, (f, h, w) in enumerate(grids):
@@ -250,6 +297,37 @@ def _stream(stream=None) -> int:
 
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
+
+
+def _bad(msg: str) -> "H3DitError":
+    return H3DitError(H3DIT_ERR_INVALID_ARG, msg)
+
+
+def _arg(dev, t, what: str, dtypes, shape=None, dense: bool = True) -> int | None:
+    """Device address of an argument of the FP4, norm and rotary calls: on the
+    context's device, of one of `dtypes`, of `shape` (None in it: any), and
+    contiguous (dense) or with contiguous rows."""
+    if t is None:
+        return None
+    if t.device != dev:
+        raise _bad(f"{what} is on {t.device}, the context on {dev}")
+    if t.dtype not in dtypes:
+        raise _bad(f"{what} has dtype {t.dtype}")
+    if shape is not None and (t.dim() != len(shape) or any(
+            w is not None and w != s for w, s in zip(shape, t.shape))):
+        raise _bad(f"{what} has shape {tuple(t.shape)}, not {shape}")
+    if dense:
+        if not t.is_contiguous():
+            raise _bad(f"{what} is not contiguous")
+    elif t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (
+            t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise _bad(f"{what} needs rows of consecutive elements that do not overlap")
+    return t.data_ptr()
+
+
+def _ld(t, width: int) -> int:
+    """Row stride of a matrix of rows (torch leaves it open for one row)."""
+    return t.stride(0) if t.shape[0] > 1 else max(width, (width + 7) // 8 * 8)
 
 
 def ipc_handle(t) -> Tuple[bytes, int]:
@@ -493,6 +571,188 @@ class Context:
         self._check(lib.h3dit_attention_mx(self.handle, _ptr(q, False), _ptr(k, False),
                                            _ptr(v, False), ld_qkv, _ptr(o), _ptr(o_sf), n,
                                            _stream(stream)))
+
+    def _here(self, stream) -> int:
+        """The stream of a call on the context's device, which has to be current."""
+        import torch
+
+        dev = self.workspace.device
+        if torch.cuda.current_device() != dev.index:
+            raise _bad(f"the context lives on {dev}, the current device is "
+                       f"cuda:{torch.cuda.current_device()}")
+        return _stream(stream)
+
+    def _scalar(self, t, what: str) -> int | None:
+        import torch
+
+        if t is not None and t.numel() != 1:
+            raise _bad(f"{what} is not one number")
+        return _arg(self.workspace.device, t, what, (torch.float32,))
+
+    def _fp4(self, fmt: int, rows: int, k: int, q, sf, what: str) -> Tuple[int, int]:
+        """Addresses of the codes [rows, k/2] and of the scales of an FP4 matrix."""
+        import torch
+
+        dev, u8 = self.workspace.device, (torch.uint8,)
+        if fmt not in (H3DIT_FP4_MX, H3DIT_FP4_NV):
+            raise _bad(f"unknown FP4 format {fmt}")
+        if q is None or sf is None:
+            raise _bad(f"{what}: codes and scales are both needed")
+        ptrs = _arg(dev, q, what, u8, (rows, k // 2)), _arg(dev, sf, what + " scales", u8)
+        if sf.numel() < fp4_scale_bytes(fmt, rows, k):
+            raise _bad(f"{what} scales: {sf.numel()} bytes, {fp4_scale_bytes(fmt, rows, k)} needed")
+        return ptrs
+
+    def _fp4_source(self, src) -> tuple:
+        import torch
+
+        ptr = _arg(self.workspace.device, src, "src", (torch.bfloat16, torch.float32), (None, None),
+                   dense=False)
+        rows, k = src.shape
+        return ptr, int(src.dtype == torch.float32), _ld(src, k), rows, k
+
+    def fp4_tensor_scale(self, src, scale_out, stream=None) -> None:
+        """scale_out (one fp32) = src's largest finite magnitude over 2688 (1 if
+        that is 0): what an NVFP4 matrix of src is quantized under."""
+        if scale_out is None:
+            raise _bad("scale_out is None")
+        self._check(lib.h3dit_fp4_tensor_scale(self.handle, *self._fp4_source(src),
+                                               self._scalar(scale_out, "scale_out"),
+                                               self._here(stream)))
+
+    def fp4_quantize(self, fmt: int, src, q, sf, tensor_scale=None, stream=None) -> None:
+        """src [rows, k] (bf16 or fp32, rows may be strided) -> codes q [rows, k/2]
+        and scales sf (fp4_scale_bytes) in format H3DIT_FP4_MX or _NV."""
+        source = self._fp4_source(src)
+        qp, sp = self._fp4(fmt, src.shape[0], src.shape[1], q, sf, "q")
+        self._check(lib.h3dit_fp4_quantize(self.handle, fmt, *source,
+                                           self._scalar(tensor_scale, "tensor_scale"), qp, sp,
+                                           self._here(stream)))
+
+    def fp4_dequantize(self, fmt: int, q, sf, out, tensor_scale=None, stream=None) -> None:
+        """The bf16 values [rows, k] of an FP4 matrix."""
+        import torch
+
+        op = _arg(self.workspace.device, out, "out", (torch.bfloat16,), (None, None))
+        rows, k = out.shape
+        qp, sp = self._fp4(fmt, rows, k, q, sf, "q")
+        self._check(lib.h3dit_fp4_dequantize(self.handle, fmt, qp, sp,
+                                             self._scalar(tensor_scale, "tensor_scale"), rows, k,
+                                             op, self._here(stream)))
+
+    def linear_fp4(self, fmt: int, epilogue: int, a, a_sf, w, w_sf, out, a_scale=None,
+                   w_scale=None, out_sf=None, out_scale=None, bias=None, gate=None, resid=None,
+                   stream=None) -> None:
+        """out = epilogue(a_scale w_scale a w^T + bias) of two FP4 matrices: a
+        codes [m, k/2], w codes [n, k/2]; see h3dit_linear_fp4."""
+        import torch
+
+        dev, f32 = self.workspace.device, (torch.float32,)
+        m, k = a.shape[0], 2 * a.shape[1]
+        n = w.shape[0]
+        ap, asp = self._fp4(fmt, m, k, a, a_sf, "a")
+        wp, wsp = self._fp4(fmt, n, k, w, w_sf, "w")
+        osp = None
+        if out_sf is not None:
+            op, osp = self._fp4(fmt, m, n, out, out_sf, "out")
+        else:
+            dt = f32 if epilogue == H3DIT_EPI_GATED_RESIDUAL else (torch.bfloat16,)
+            op = _arg(dev, out, "out", dt, (m, n))
+        self._check(lib.h3dit_linear_fp4(
+            self.handle, fmt, epilogue, ap, asp, self._scalar(a_scale, "a_scale"), wp, wsp,
+            self._scalar(w_scale, "w_scale"), m, n, k, op, osp,
+            self._scalar(out_scale, "out_scale"), _arg(dev, bias, "bias", f32, (n,)),
+            _arg(dev, gate, "gate", f32, (n,)), _arg(dev, resid, "resid", f32, (m, n)),
+            self._here(stream)))
+
+    def gated_norm(self, x, x_out, out_kind: int, out, out_sf=None, out_scale=None, branch=None,
+                   gate=None, shift=None, scale=None, rows_per_group: int = 0,
+                   post_norm: bool = False, post_weight=None, pre_weight=None,
+                   residual_scale: float = 1.0, stream=None) -> None:
+        """x_out = residual_scale x + gate * (post_norm ? RMSNorm(branch) post_weight
+        : branch); out = RMSNorm(x_out) pre_weight (1 + scale) + shift as bf16,
+        MXFP8 or FP4. gate, shift and scale are [D], or [groups, D] with equal row
+        strides for rows_per_group rows each."""
+        import torch
+
+        dev, f32, D = self.workspace.device, (torch.float32,), self.cfg.hidden
+        if x is None or out is None:
+            raise _bad("x and out are needed")
+        xp = _arg(dev, x, "x", f32, (None, D))
+        n = x.shape[0]
+        groups = 1
+        if rows_per_group < 0:
+            raise _bad("rows_per_group < 0")
+        if rows_per_group > 0:
+            groups = max(1, -(-n // rows_per_group))
+        ld, mods = None, []
+        for name, t in (("gate", gate), ("shift", shift), ("scale", scale)):
+            if t is None:
+                mods.append(None)
+            elif t.dim() == 1:
+                if groups > 1:
+                    raise _bad(f"{name} has one row for {groups} groups")
+                mods.append(_arg(dev, t, name, f32, (D,)))
+            else:
+                mods.append(_arg(dev, t, name, f32, (None, D), dense=False))
+                if t.shape[0] < groups:
+                    raise _bad(f"{name} has {t.shape[0]} rows for {groups} groups")
+                if groups > 1:
+                    if ld is not None and ld != t.stride(0):
+                        raise _bad("gate, shift and scale need equal row strides")
+                    ld = t.stride(0)
+        if out_kind in (H3DIT_NORM_OUT_FP4_MX, H3DIT_NORM_OUT_FP4_NV):
+            fmt = H3DIT_FP4_MX if out_kind == H3DIT_NORM_OUT_FP4_MX else H3DIT_FP4_NV
+            op, sp = self._fp4(fmt, n, D, out, out_sf, "out")
+        elif out_kind == H3DIT_NORM_OUT_MXFP8:
+            op, sp = (_arg(dev, out, "out", (torch.uint8,)),
+                      _arg(dev, out_sf, "out_sf", (torch.uint8,)))
+            if out.numel() != n * D or out_sf is None or out_sf.numel() < mx_scale_bytes(n, D):
+                raise _bad("MXFP8 output: out or out_sf has the wrong size")
+        else:
+            op = _arg(dev, out, "out", (torch.bfloat16,), (n, D))
+            sp = _arg(dev, out_sf, "out_sf", (torch.uint8,))
+        args = h3dit_norm_args(
+            xp, _arg(dev, x_out, "x_out", f32, (n, D)),
+            _arg(dev, branch, "branch", (torch.bfloat16, torch.float32), (n, D)),
+            int(branch is not None and branch.dtype == torch.float32), int(post_norm),
+            _arg(dev, post_weight, "post_weight", f32, (D,)),
+            _arg(dev, pre_weight, "pre_weight", f32, (D,)), mods[0], mods[1], mods[2],
+            0 if ld is None else ld, n, rows_per_group, residual_scale, out_kind, op, sp,
+            self._scalar(out_scale, "out_scale"))
+        self._check(lib.h3dit_gated_norm(self.handle, C.byref(args), self._here(stream)))
+
+    def rope_axes(self, spec: h3dit_rope_spec, positions, q, q_out, heads_q: int, k=None,
+                  k_out=None, heads_k: int = 0, q_weight=None, k_weight=None,
+                  inverse: bool = False, stream=None) -> None:
+        """q [n, heads_q * head_dim] and k [n, heads_k * head_dim] (bf16 or fp32,
+        rows may be strided) turned by positions [n, 3] into q_out and k_out;
+        with a weight both are RMS-normalised per head first."""
+        import torch
+
+        dev, f32 = self.workspace.device, (torch.float32,)
+        if positions is None or positions.dim() != 2:
+            raise _bad("positions must be [n, 3]")
+        n, dh = positions.shape[0], spec.head_dim
+        sides, dt = [], None
+        for name, t, o, heads in (("q", q, q_out, heads_q), ("k", k, k_out, heads_k)):
+            if heads <= 0:
+                sides.append((None, 0, None, 0, heads))
+                continue
+            if t is None or o is None:
+                raise _bad(f"{name} and {name}_out are needed")
+            dt = dt or t.dtype
+            types = (dt,) if dt in (torch.bfloat16, torch.float32) else ()
+            sides.append((_arg(dev, t, name, types, (n, heads * dh), dense=False),
+                          _ld(t, heads * dh),
+                          _arg(dev, o, name + "_out", types, (n, heads * dh), dense=False),
+                          _ld(o, heads * dh), heads))
+        self._check(lib.h3dit_rope_axes(
+            self.handle, C.byref(spec), _arg(dev, positions, "positions", f32, (None, 3)), n,
+            int(dt == torch.float32), *sides[0], *sides[1],
+            _arg(dev, q_weight, "q_weight", f32, (dh,)),
+            _arg(dev, k_weight, "k_weight", f32, (dh,)),
+            H3DIT_ROPE_INVERSE if inverse else 0, self._here(stream)))
 
     def embed_latent(self, latent, w_in, b_in, x_img_out, stream=None) -> None:
         """latent fp32 [C, Hl, Wl] -> x_img_out [(Hl/2)(Wl/2), D] in the token dtype."""

@@ -47,7 +47,8 @@ typedef int32_t h3dit_status;
 
 /* Empty inputs: a stage call whose row or token count is 0 (m of the
  * linears, n of the norms and the attention, n_local / n_total of the
- * sequence-parallel calls, rows of h3dit_mx_quantize, an empty RoPE table)
+ * sequence-parallel calls, rows of h3dit_mx_quantize, of the FP4 calls and of
+ * h3dit_gated_norm, n of h3dit_rope_axes, an empty RoPE table)
  * checks its counts and shape arguments, then returns H3DIT_OK without
  * launching anything or examining its data pointers, which may be NULL. */
 
@@ -410,6 +411,142 @@ h3dit_status h3dit_rmsnorm_modulate_mx(h3dit_ctx *ctx, const float *x, const flo
 h3dit_status h3dit_attention_mx(h3dit_ctx *ctx, const void *q, const void *k, const void *v,
                                 int32_t ld_qkv, void *o, void *o_sf, int32_t n, void *cuda_stream);
 
+/* ---- 4-bit matrices, the norms around a branch, rotary axes -------------
+ * The next step below MXFP8 for a block's linears, with what runs between
+ * them: gated_norm (FP4 rows out) -> linear_fp4 (QKV) -> rope_axes (the norm of
+ * Q and K heads and their rotation) -> attention -> fp4_quantize -> linear_fp4
+ * -> gated_norm -> linear_fp4 (GELU, FP4 rows out) -> linear_fp4.
+ * These calls work on the device that was current in h3dit_create, which has to
+ * be current when they are made (H3DIT_ERR_INVALID_ARG otherwise).
+ *
+ * An FP4 matrix [rows, k], k a multiple of 64, is
+ *   codes   device uint8 [rows, k/2]: E2M1 (0, .5, 1, 1.5, 2, 3, 4, 6 and their
+ *           negatives), the even column in the low half of a byte;
+ *   scales  device uint8, h3dit_fp4_scale_bytes bytes: one per block of
+ *           consecutive columns, S = k / block of a row. The scale of row r and
+ *           block s is byte ((r / 128) * ceil(S / 4) + s / 4) * 512 +
+ *           (r % 32) * 16 + (r / 32 % 4) * 4 + s % 4. What no row or block owns
+ *           is never used; scales of blocks past a row's last, where their group
+ *           of four has them, are written as 0, rows past the last are left;
+ *   H3DIT_FP4_MX  block 32, E8M0 scale 2^X with X = floor(log2(amax)) - 2, at
+ *           least 2^-127, elements E2M1(x 2^-X);
+ *   H3DIT_FP4_NV  block 16, E4M3 scale s = E4M3(fl(amax fl(1 / fl(6 g)))) under
+ *           one fp32 scale g > 0 of the whole tensor, elements
+ *           E2M1(fl(x fl(1 / d))), d = fl(s g); all 0 where d < 2^-126;
+ * every rounding to nearest even and saturating, fl() to fp32. A block with a
+ * NaN or an infinity (and every NVFP4 block if g is not positive and finite)
+ * gets the scale format's NaN and stands for NaN. */
+#define H3DIT_FP4_MX 0
+#define H3DIT_FP4_NV 1
+
+/* Bytes of the scale array (0 for an unknown format, rows <= 0 or a k that is
+ * not a positive multiple of 64). */
+size_t h3dit_fp4_scale_bytes(int32_t format, int32_t rows, int32_t k);
+
+/* *scale_out (device fp32) = largest finite magnitude of src over 2688 = 6 * 448,
+ * or 1 for a matrix of zeros: the tensor scale of src in NVFP4. src: device bf16
+ * [rows, k], fp32 if src_fp32 is 1, k a multiple of 64, row stride ld elements (a
+ * multiple of 16 bytes). rows 0 leaves *scale_out as it is. Uses the context's
+ * workspace. */
+h3dit_status h3dit_fp4_tensor_scale(h3dit_ctx *ctx, const void *src, int32_t src_fp32, int64_t ld,
+                                    int32_t rows, int32_t k, float *scale_out, void *cuda_stream);
+
+/* src (as above) -> codes and scales. tensor_scale: device fp32 scalar g of
+ * H3DIT_FP4_NV (NULL means 1); NULL with H3DIT_FP4_MX. */
+h3dit_status h3dit_fp4_quantize(h3dit_ctx *ctx, int32_t format, const void *src, int32_t src_fp32,
+                                int64_t ld, int32_t rows, int32_t k, const float *tensor_scale,
+                                void *codes, void *scales, void *cuda_stream);
+
+/* codes and scales -> out device bf16 [rows, k]: element * scale (* g, NULL
+ * means 1, with either format), in fp32, rounded once. */
+h3dit_status h3dit_fp4_dequantize(h3dit_ctx *ctx, int32_t format, const void *codes,
+                                  const void *scales, const float *tensor_scale, int32_t rows,
+                                  int32_t k, void *out, void *cuda_stream);
+
+/* FP4 linear: v = (a_scale w_scale) sum_k A W + bias with A [m, k] and W [n, k]
+ * FP4 matrices of one format, fp32 accumulation; k a multiple of 64, n of 32.
+ * a_scale, w_scale: device fp32 scalars or NULL for 1; bias: device fp32 [n] or
+ * NULL. Epilogues:
+ *   STORE           out device bf16 [m, n] = v
+ *   GELU            out device bf16 [m, n] = GELU(v); with out_sf not NULL an FP4
+ *                   matrix of the operands' format instead (out codes [m, n/2],
+ *                   n a multiple of 64), under out_scale for H3DIT_FP4_NV
+ *                   (device fp32 scalar, NULL means 1)
+ *   GATED_RESIDUAL  out device fp32 [m, n] = resid + gate[col] v; resid device
+ *                   fp32 [m, n], may be out, and is out where NULL
+ * QKV_ROPE is not offered (h3dit_rope_axes follows a STORE). */
+h3dit_status h3dit_linear_fp4(h3dit_ctx *ctx, int32_t format, int32_t epilogue, const void *a,
+                              const void *a_sf, const float *a_scale, const void *w,
+                              const void *w_sf, const float *w_scale, int32_t m, int32_t n,
+                              int32_t k, void *out, void *out_sf, const float *out_scale,
+                              const float *bias, const float *gate, const float *resid,
+                              void *cuda_stream);
+
+/* What h3dit_gated_norm writes. */
+#define H3DIT_NORM_OUT_BF16 0
+#define H3DIT_NORM_OUT_MXFP8 1  /* hidden a multiple of 128, scales as h3dit_mx_quantize's */
+#define H3DIT_NORM_OUT_FP4_MX 2
+#define H3DIT_NORM_OUT_FP4_NV 3
+
+typedef struct h3dit_norm_args {
+  const float *x;           /* device fp32 [rows, D]: the residual stream               */
+  float *x_out;             /* device fp32 [rows, D] or NULL (not written); may be x    */
+  const void *branch;       /* device [rows, D], bf16 or fp32, or NULL for no branch    */
+  int32_t branch_fp32;      /* 0 bf16, 1 fp32                                           */
+  int32_t post_norm;        /* 1: RMSNorm of the branch before its gate                 */
+  const float *post_weight; /* device fp32 [D] or NULL (1); only with post_norm         */
+  const float *pre_weight;  /* device fp32 [D] or NULL (1)                              */
+  const float *gate;        /* device fp32, one row of D per group, or NULL (1)         */
+  const float *shift;       /* the same, or NULL (0)                                    */
+  const float *scale;       /* the same, or NULL (0)                                    */
+  int64_t ld_mod;           /* floats from a group's row of gate, shift and scale to the
+                               next, a multiple of 4 (unused with one group)            */
+  int32_t rows;
+  int32_t rows_per_group;   /* rows [g * this, (g + 1) * this) are group g; 0: one group */
+  float residual_scale;     /* r                                                        */
+  int32_t out_kind;         /* H3DIT_NORM_OUT_*                                         */
+  void *out;                /* bf16 / E4M3 [rows, D], or FP4 codes [rows, D/2]          */
+  void *out_sf;             /* scales of the MXFP8 and FP4 outputs                      */
+  const float *out_scale;   /* device fp32 scalar of FP4_NV, NULL means 1               */
+} h3dit_norm_args;
+
+/* The norms on either side of a residual addition, in one pass per row:
+ *   x' = r x + gate * (post_norm ? RMSNorm(branch) post_weight : branch)
+ *   out = RMSNorm(x') pre_weight (1 + scale) + shift
+ * with RMSNorm(v) = v / sqrt(mean(v^2) + norm_eps); x' in fp32, out rounded once
+ * to its kind. D is the context's hidden. A row with a NaN is NaN in both. */
+h3dit_status h3dit_gated_norm(h3dit_ctx *ctx, const h3dit_norm_args *args, void *cuda_stream);
+
+/* Rotary positions on three axes: the head's first 2 (s0 + s1 + s2) elements
+ * turn, s_i pairs by axis i, the rest pass through. Pair j of axis i turns by
+ * position_i * theta^(-j / s_i). */
+typedef struct h3dit_rope_spec {
+  int32_t head_dim;    /* a multiple of 16, 16 .. 256                                   */
+  int32_t sections[3]; /* pairs per axis, >= 0, 2 * sum <= head_dim                     */
+  float theta;         /* > 0, finite                                                   */
+  int32_t interleaved; /* 1: a pair is two neighbours; 0: elements j and s_i + j of
+                          axis i's 2 s_i elements (as h3dit_rope_table's users)         */
+} h3dit_rope_spec;
+
+#define H3DIT_ROPE_INVERSE 1 /* flags: turn back (also the rotation's gradient) */
+
+/* q [n, heads_q * head_dim] and k [n, heads_k * head_dim], device bf16 (fp32 if
+ * io_fp32 is 1) with row strides ld_q, ld_k elements (multiples of 16 bytes) ->
+ * q_out, k_out of the same type with row strides ld_q_out, ld_k_out; each output
+ * may be its input with the same stride (else they must not overlap). positions:
+ * device fp32 [n, 3], fractions and negative ones too; an angle is good to about
+ * 1e-7 for positions up to 1e6. q_weight, k_weight: device fp32 [head_dim]: with
+ * either not NULL both Q and K heads are RMS-normalised (norm_eps) before they
+ * turn, by the weight that is given, or 1. heads_q or heads_k may be 0 (its
+ * pointers are then not examined). A weight with H3DIT_ROPE_INVERSE is
+ * H3DIT_ERR_INVALID_ARG. */
+h3dit_status h3dit_rope_axes(h3dit_ctx *ctx, const h3dit_rope_spec *spec, const float *positions,
+                             int32_t n, int32_t io_fp32, const void *q, int64_t ld_q, void *q_out,
+                             int64_t ld_q_out, int32_t heads_q, const void *k, int64_t ld_k,
+                             void *k_out, int64_t ld_k_out, int32_t heads_k,
+                             const float *q_weight, const float *k_weight, int32_t flags,
+                             void *cuda_stream);
+
 /* ---- Around the block loop: latent in, velocity out, sampler step --------
  * MiniMax-H3-Image model card, "Model Architecture": the image VAE's latent
  * has 24 channels at 16x spatial downsampling; the DiT patchifies it with a
@@ -634,7 +771,11 @@ h3dit_status h3dit_selftest_bounded_wait(h3dit_ctx *ctx, int32_t limit_us, void 
 #define H3DIT_KERNEL_PACK 9       /* packing / unpacking tokens    */
 #define H3DIT_KERNEL_MX_QUANTIZE 10 /* h3dit_mx_quantize           */
 #define H3DIT_KERNEL_IO 11        /* patch embedding, output layer + Euler */
-#define H3DIT_KERNEL_COUNT 12
+#define H3DIT_KERNEL_FP4_QUANTIZE 12 /* tensor scale, quantization, values */
+#define H3DIT_KERNEL_LINEAR_FP4 13 /* h3dit_linear_fp4            */
+#define H3DIT_KERNEL_GATED_NORM 14 /* h3dit_gated_norm            */
+#define H3DIT_KERNEL_ROPE_AXES 15 /* h3dit_rope_axes              */
+#define H3DIT_KERNEL_COUNT 16
 
 /* Start recording a CUDA event pair around every kernel the context launches
  * (on the stream it is launched on), dropping earlier records. */
