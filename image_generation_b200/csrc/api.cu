@@ -1754,23 +1754,36 @@ h3dit_status run_linear_fp4(h3dit_ctx *ctx, int format, int epi, Fp4GemmParams &
   EncodeTiledFn fn = encode_fn();
   if (!fn) return ctx->fail(H3DIT_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   const int kernel_epi = epi == H3DIT_EPI_GELU && p.out_sf ? static_cast<int>(kEpiGeluFp4) : epi;
-  const Fp4GemmPlan plan = fp4_gemm_plan(format, kernel_epi, &p, ctx->num_sms);
-  CUtensorMap ta, tb;
-  // rows of packed bytes, read in boxes of 128 bytes; past the row's end they read 0
-  auto encode = [&](CUtensorMap *t, const void *base, int rows, int box) {
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(p.k / 2), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(p.k / 2)};
-    const cuuint32_t boxes[2] = {128, static_cast<cuuint32_t>(box)};
+  const Fp4GemmPlan plan = fp4_gemm_plan(format, &p, ctx->num_sms);
+  Fp4GemmMaps t;
+  auto encode = [&](CUtensorMap *m, CUtensorMapDataType type, const void *base, uint64_t row_bytes,
+                    int elem, int rows, int box, int box_rows, CUtensorMapSwizzle swizzle) {
+    const cuuint64_t dims[2] = {row_bytes / elem, static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {row_bytes};
+    const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t estr[2] = {1, 1};
-    return fn(t, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, boxes,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return fn(m, type, 2, const_cast<void *>(base), dims, strides, boxes, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
-  CUresult r = encode(&ta, a, p.m, plan.box_a);
-  if (r == CUDA_SUCCESS) r = encode(&tb, w, p.n, plan.box_b);
+  // codes: past a row's end they read 0
+  auto codes = [&](CUtensorMap *m, const void *base, int rows, int box_rows) {
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, p.k / 2, 1, rows, 128, box_rows,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
+  };
+  // scales: the 512-byte blocks of a k-block (256 columns), of one or two row blocks
+  auto scales = [&](CUtensorMap *m, const void *base, int rows, int box_rows) {
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_INT64, base, static_cast<uint64_t>(p.chunks) * 512, 8,
+                  (rows + 127) / 128, 64 * 64 / fp4_block(format), box_rows,
+                  CU_TENSOR_MAP_SWIZZLE_NONE);
+  };
+  CUresult r = codes(&t.a, a, p.m, plan.box_a);
+  if (r == CUDA_SUCCESS) r = codes(&t.b, w, p.n, plan.box_b);
+  if (r == CUDA_SUCCESS && plan.pair) r = scales(&t.a_sf, p.a_sf, p.m, 1);
+  if (r == CUDA_SUCCESS && plan.pair) r = scales(&t.b_sf, p.b_sf, p.n, 2);
   if (r != CUDA_SUCCESS) return ctx->fail(H3DIT_ERR_CUDA, "tensor map encode failed (%d)", (int)r);
   Launch L(ctx, H3DIT_KERNEL_LINEAR_FP4, s);
-  return ctx->cuda(launch_gemm_fp4(format, kernel_epi, ta, tb, p, plan, s), "FP4 gemm launch");
+  return ctx->cuda(launch_gemm_fp4(format, kernel_epi, t, p, plan, s), "FP4 gemm launch");
 }
 
 }  // namespace

@@ -323,24 +323,316 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const Fp4GemmPara
 }
 }  // namespace one
 
+// ------------------------------------------------------- a pair of CTAs per tile
+// Output tiles of 256 x 192 on clusters of two CTAs (M256 N192 K64): each CTA
+// loads its own 128 rows of A and 96 of W's 192, so a byte from L2 feeds nearly
+// twice the MACs of a one-CTA tile. 2 x 192 columns of tensor memory hold two
+// accumulators, the other 128 the scales of SLOTS k-blocks: a slot is written
+// again once the MMAs that read it have completed (its k-block's EMPTY phase).
+// 192 columns start at 0 or 64 in a block of 128 scale rows; both blocks that
+// they touch are copied, and an odd tile's MMAs read them from column 2 on.
+namespace pair {
+constexpr int BN = 192;
+constexpr int PARTS = 2;  // epilogue warps per TMEM lane quarter
+constexpr int THREADS = 64 + 128 * PARTS;
+constexpr int STAGES = 5;
+constexpr int A_BYTES = BM * BKB, B_BYTES = BN / 2 * BKB;
+constexpr uint16_t kBothCtas = 0x3, kFirstCta = 0x1;
+
+template <int FMT>
+struct Tile {
+  static constexpr int SFA_BYTES = Kb<FMT>::CHUNKS * SF, SFB_BYTES = 2 * SFA_BYTES;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
+  static constexpr int NUM_BARS = 2 * STAGES + 4 + 1;
+  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + NUM_BARS * 8 + 16;
+  static constexpr uint32_t SF_COL0 = 2 * BN;
+  static constexpr uint32_t SF_COLS = 12 * Kb<FMT>::CHUNKS;
+  static constexpr int FIT = static_cast<int>((TMEM_COLS - SF_COL0) / SF_COLS);
+  static constexpr int SLOTS = FIT < STAGES ? FIT : STAGES;
+};
+static_assert(Tile<kFp4Nv>::SLOTS >= 2 && Tile<kFp4Mx>::SLOTS >= 2, "TMEM budget");
+static_assert(Tile<kFp4Nv>::STAGE_BYTES % 1024 == 0 && Tile<kFp4Mx>::STAGE_BYTES % 1024 == 0,
+              "stages start on swizzle atoms");
+static_assert(Tile<kFp4Nv>::SMEM_BYTES <= 227 * 1024, "shared memory budget");
+
 template <int FMT, int EPI>
-cudaError_t launch_epi(const CUtensorMap &a, const CUtensorMap &b, const Fp4GemmParams &p,
-                       const Fp4GemmPlan &plan, cudaStream_t s) {
-  return one::launch<FMT, EPI>(a, b, p, plan.grid, s);
+__global__ void __launch_bounds__(THREADS, 1)
+    gemm_fp4_pair(const __grid_constant__ CUtensorMap tma_a,
+                  const __grid_constant__ CUtensorMap tma_b,
+                  const __grid_constant__ CUtensorMap tma_sfa,
+                  const __grid_constant__ CUtensorMap tma_sfb, const Fp4GemmParams p) {
+  using T = Tile<FMT>;
+  constexpr bool NV = FMT == kFp4Nv;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * T::STAGE_BYTES);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + T::NUM_BARS);
+  __shared__ int entry_status;
+  __shared__ int loads_issued;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const uint32_t peer = rank ^ 1u;
+  const bool leader = rank == 0;
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar0 = smem_u32(bars);
+  auto FULL = [&](int s) { return bar0 + 8u * s; };
+  auto EMPTY = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto TFULL = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
+  auto TEMPTY = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
+  const uint32_t DRAIN = bar0 + 8u * (2 * STAGES + 4);
+
+  if (threadIdx.x == 0) {
+    entry_status = *reinterpret_cast<const volatile int *>(p.status);
+    loads_issued = 0;
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(FULL(s), 2);  // one arrival per producer of the pair
+      mbar_init(EMPTY(s), 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(TFULL(a), 1);
+      mbar_init(TEMPTY(a), 2 * 128 * PARTS);  // both CTAs' epilogue threads
+    }
+    mbar_init(DRAIN, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tma_a);
+    tma_prefetch_desc(&tma_b);
+    tma_prefetch_desc(&tma_sfa);
+    tma_prefetch_desc(&tma_sfb);
+  }
+  cluster_sync();  // barriers initialised and entry status visible pair-wide
+  const int peer_status =
+      static_cast<int>(ld_shared_cluster_u32(map_to_cta(smem_u32(&entry_status), peer)));
+  const bool skip = (entry_status | peer_status) != 0;
+  if (!skip && warp == 1) {
+    tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();  // the peer has read our status word; TMEM allocated in both
+  if (skip) return;
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int num_tiles = p.tiles_m * p.tiles_n;
+  const int kblocks = (p.k + BK - 1) / BK;
+  const int pair_id = blockIdx.x >> 1;
+  const int pairs = gridDim.x >> 1;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const uint32_t full_leader = map_to_cta(FULL(0), 0);
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;
+      bool ok = true;
+      for (int t = pair_id; t < num_tiles && ok; t += pairs) {
+        int tm, tn;
+        tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
+        const int block_a = 2 * tm + static_cast<int>(rank);
+        const int row_b = tn * BN + static_cast<int>(rank) * (BN / 2);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait(EMPTY(stage), phase ^ 1, p.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full = full_leader + 8u * stage;
+          // boxes count whole, also where they read past a matrix
+          if (leader)
+            mbar_arrive_expect_tx(FULL(stage), T::STAGE_BYTES);
+          else
+            mbar_arrive_expect_tx_cluster(full, T::STAGE_BYTES);
+          const uint32_t sa = sbase + stage * T::STAGE_BYTES;
+          const int sf_x = kb * (T::SFA_BYTES / 8);  // 8-byte elements
+          tma_load_2d_pair(sa, &tma_a, kb * BKB, block_a * BM, full);
+          tma_load_2d_pair(sa + A_BYTES, &tma_b, kb * BKB, row_b, full);
+          tma_load_2d_pair(sa + A_BYTES + B_BYTES, &tma_sfa, sf_x, block_a, full);
+          tma_load_2d_pair(sa + A_BYTES + B_BYTES + T::SFA_BYTES, &tma_sfb, sf_x, tn * BN / 128,
+                           full);
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      loads_issued = issued;
+    }
+  } else if (warp == 1) {
+    if (leader) {
+      int stage = 0, slot = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      int used = 0;  // slots written so far, up to SLOTS
+      bool ok = true;
+      for (int t = pair_id; t < num_tiles && ok; t += pairs) {
+        int tm, tn;
+        tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
+        const uint32_t odd = 2u * (tn & 1);
+        ok = mbar_wait_cluster(TEMPTY(acc), acc_phase ^ 1, p.status);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
+        for (int kb = 0; kb < kblocks; ++kb) {
+          ok = mbar_wait_warp(FULL(stage), phase, p.status);
+          if (!ok) break;
+          if (T::SLOTS < STAGES && used == T::SLOTS) {
+            const bool wrapped = stage < T::SLOTS;  // the k-block SLOTS before this one
+            ok = mbar_wait_warp(EMPTY(wrapped ? stage - T::SLOTS + STAGES : stage - T::SLOTS),
+                                wrapped ? phase ^ 1 : phase, p.status);
+            if (!ok) break;
+          }
+          tc_fence_after();
+          const uint32_t sa = sbase + stage * T::STAGE_BYTES;
+          const uint64_t da = desc_sw128(sa, 16, 1024), db = desc_sw128(sa + A_BYTES, 16, 1024);
+          const uint64_t dsf = desc_sf_copy(sa + A_BYTES + B_BYTES);
+          const uint32_t sfa = tmem + T::SF_COL0 + T::SF_COLS * slot;
+          const uint32_t sfb = sfa + 4 * Kb<FMT>::CHUNKS;
+          const int groups = min(4, (p.k - kb * BK) / 64);
+          if (elect_one()) {
+            // descriptors count in 16 bytes; nothing here carries out of the address
+#pragma unroll
+            for (int c = 0; c < Kb<FMT>::CHUNKS; ++c) {
+              if (c * Kb<FMT>::PER_CHUNK >= groups) break;
+              tmem_cp_sf_pair(sfa + 4 * c, dsf + c * SF / 16);
+              tmem_cp_sf_pair(sfb + 8 * c, dsf + (T::SFA_BYTES + c * SF) / 16);
+              tmem_cp_sf_pair(sfb + 8 * c + 4, dsf + (2 * T::SFA_BYTES + c * SF) / 16);
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              if (g >= groups) break;
+              const int c = g / Kb<FMT>::PER_CHUNK, id = 2 * (g % Kb<FMT>::PER_CHUNK);
+              umma_fp4_pair<NV>(d, da + 2 * g, db + 2 * g, idesc_fp4(2 * BM, BN, NV, id),
+                                sfa + 4 * c, sfb + 8 * c + odd, (kb | g) != 0 ? 1u : 0u);
+            }
+            umma_commit_pair(EMPTY(stage), kBothCtas);
+          }
+          __syncwarp();
+          if (used < T::SLOTS) ++used;
+          if (++slot == T::SLOTS) slot = 0;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (elect_one()) umma_commit_pair(TFULL(acc), kBothCtas);
+        __syncwarp();
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      }
+      // Every pair MMA (and the arrivals its commits make) completes before
+      // either CTA may release TMEM or exit.
+      if (elect_one()) umma_commit_pair(DRAIN, kFirstCta);
+      __syncwarp();
+      mbar_wait(DRAIN, 0, p.status, false);
+    }
+  } else {
+    const int sub = warp & 3;  // TMEM lane quarter this warp may access
+    const int part = (warp - 2) >> 2;
+    const Alpha al = tensor_alpha(p.a_scale, p.b_scale);
+    const uint32_t tempty_leader = map_to_cta(TEMPTY(0), 0);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int t = pair_id; t < num_tiles; t += pairs) {
+      int tm, tn;
+      tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
+      const bool ok = mbar_wait(TFULL(acc), acc_phase, p.status);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const uint32_t tbase =
+          tmem + (static_cast<uint32_t>(sub * 32) << 16) + static_cast<uint32_t>(acc * BN);
+      const int row = (2 * tm + static_cast<int>(rank)) * BM + sub * 32 + lane;
+#pragma unroll 1
+      for (int c = 32 * part; c < BN && tn * BN + c < p.n; c += 32 * PARTS) {
+        uint32_t r[32];
+        tmem_ld32(tbase + c, r);
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+        if (row < p.m) finish32<FMT, EPI>(p, al, v, row, tn * BN + c);
+      }
+      tc_fence_before();
+      if (leader)
+        mbar_arrive(TEMPTY(acc));
+      else
+        mbar_arrive_cluster(tempty_leader + 8u * acc);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1;
+    }
+  }
+
+  // Drain: every load either producer issued must land before its CTA exits.
+  // A stage's FULL phase completes once both producers arrived and all bytes
+  // landed; where one producer stopped early (after a failure elsewhere) the
+  // first CTA arrives in its place, then waits out the last STAGES loads.
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  if (leader && threadIdx.x == 0) {
+    const int mine = loads_issued;
+    const int theirs =
+        static_cast<int>(ld_shared_cluster_u32(map_to_cta(smem_u32(&loads_issued), peer)));
+    const int lo = mine < theirs ? mine : theirs;
+    const int hi = mine < theirs ? theirs : mine;
+    for (int i = lo; i < hi; ++i) mbar_arrive(FULL(i % STAGES));
+    for (int i = hi - STAGES > 0 ? hi - STAGES : 0; i < hi; ++i)
+      mbar_wait(FULL(i % STAGES), (i / STAGES) & 1, p.status, false);
+  }
+  __syncwarp();
+  cluster_sync();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, TMEM_COLS);
+  }
+}
+
+template <int FMT, int EPI>
+cudaError_t launch(const Fp4GemmMaps &t, const Fp4GemmParams &p, int grid, cudaStream_t s) {
+  static PerDevice smem_attr;
+  cudaError_t e = set_smem_once(smem_attr, gemm_fp4_pair<FMT, EPI>, Tile<FMT>::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = Tile<FMT>::SMEM_BYTES;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemm_fp4_pair<FMT, EPI>, t.a, t.b, t.a_sf, t.b_sf, p);
+}
+}  // namespace pair
+
+template <int FMT, int EPI>
+cudaError_t launch_epi(const Fp4GemmMaps &t, const Fp4GemmParams &p, const Fp4GemmPlan &plan,
+                       cudaStream_t s) {
+  return plan.pair ? pair::launch<FMT, EPI>(t, p, plan.grid, s)
+                   : one::launch<FMT, EPI>(t.a, t.b, p, plan.grid, s);
 }
 
 template <int FMT>
-cudaError_t launch_fmt(int epi, const CUtensorMap &a, const CUtensorMap &b, const Fp4GemmParams &p,
+cudaError_t launch_fmt(int epi, const Fp4GemmMaps &t, const Fp4GemmParams &p,
                        const Fp4GemmPlan &plan, cudaStream_t s) {
   switch (epi) {
     case kEpiStore:
-      return launch_epi<FMT, kEpiStore>(a, b, p, plan, s);
+      return launch_epi<FMT, kEpiStore>(t, p, plan, s);
     case kEpiGelu:
-      return launch_epi<FMT, kEpiGelu>(a, b, p, plan, s);
+      return launch_epi<FMT, kEpiGelu>(t, p, plan, s);
     case kEpiGatedResidual:
-      return launch_epi<FMT, kEpiGatedResidual>(a, b, p, plan, s);
+      return launch_epi<FMT, kEpiGatedResidual>(t, p, plan, s);
     case kEpiGeluFp4:
-      return launch_epi<FMT, kEpiGeluFp4>(a, b, p, plan, s);
+      return launch_epi<FMT, kEpiGeluFp4>(t, p, plan, s);
     default:
       return cudaErrorInvalidValue;
   }
@@ -348,23 +640,26 @@ cudaError_t launch_fmt(int epi, const CUtensorMap &a, const CUtensorMap &b, cons
 
 }  // namespace
 
-Fp4GemmPlan fp4_gemm_plan(int fmt, int epilogue, Fp4GemmParams *p, int num_sms) {
-  (void)epilogue;
+Fp4GemmPlan fp4_gemm_plan(int fmt, Fp4GemmParams *p, int num_sms) {
   Fp4GemmPlan plan{};
   p->chunks = fp4_chunks(fmt, p->k);
-  p->tiles_m = (p->m + BM - 1) / BM;
-  p->tiles_n = (p->n + one::BN - 1) / one::BN;
+  // more than one block of 128 rows: pairs, which halve W's traffic per SM
+  plan.pair = p->m > BM;
   plan.box_a = BM;
-  plan.box_b = one::BN;
+  plan.box_b = plan.pair ? pair::BN / 2 : one::BN;
+  const int bm = plan.pair ? 2 * BM : BM, bn = plan.pair ? pair::BN : one::BN;
+  p->tiles_m = (p->m + bm - 1) / bm;
+  p->tiles_n = (p->n + bn - 1) / bn;
   const long long tiles = static_cast<long long>(p->tiles_m) * p->tiles_n;
-  plan.grid = static_cast<int>(tiles < num_sms ? tiles : num_sms);
+  const int most = plan.pair ? num_sms / 2 : num_sms;
+  plan.grid = static_cast<int>(tiles < most ? tiles : most) * (plan.pair ? 2 : 1);
   return plan;
 }
 
-cudaError_t launch_gemm_fp4(int fmt, int epilogue, const CUtensorMap &a, const CUtensorMap &b,
-                            const Fp4GemmParams &p, const Fp4GemmPlan &plan, cudaStream_t s) {
-  return fmt == kFp4Mx ? launch_fmt<kFp4Mx>(epilogue, a, b, p, plan, s)
-                       : launch_fmt<kFp4Nv>(epilogue, a, b, p, plan, s);
+cudaError_t launch_gemm_fp4(int fmt, int epilogue, const Fp4GemmMaps &t, const Fp4GemmParams &p,
+                            const Fp4GemmPlan &plan, cudaStream_t s) {
+  return fmt == kFp4Mx ? launch_fmt<kFp4Mx>(epilogue, t, p, plan, s)
+                       : launch_fmt<kFp4Nv>(epilogue, t, p, plan, s);
 }
 
 }  // namespace h3

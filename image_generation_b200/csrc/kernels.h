@@ -245,9 +245,14 @@ struct Fp4GemmPlan {
   int box_a, box_b, grid;
   bool pair;
 };
-Fp4GemmPlan fp4_gemm_plan(int fmt, int epilogue, Fp4GemmParams *p, int num_sms);
-cudaError_t launch_gemm_fp4(int fmt, int epilogue, const CUtensorMap &a, const CUtensorMap &b,
-                            const Fp4GemmParams &p, const Fp4GemmPlan &plan, cudaStream_t s);
+Fp4GemmPlan fp4_gemm_plan(int fmt, Fp4GemmParams *p, int num_sms);
+// Codes as rows of bytes in boxes of 128 bytes; for a pair also the scale
+// arrays, as rows of 8-byte elements (a row: the scale blocks of 128 rows).
+struct Fp4GemmMaps {
+  CUtensorMap a, b, a_sf, b_sf;
+};
+cudaError_t launch_gemm_fp4(int fmt, int epilogue, const Fp4GemmMaps &t, const Fp4GemmParams &p,
+                            const Fp4GemmPlan &plan, cudaStream_t s);
 
 // x_out = residual_scale x + gate * (post ? RMSNorm(branch) post_weight : branch);
 // out = RMSNorm(x_out) pre_weight (1 + scale) + shift (gated_norm.cu).

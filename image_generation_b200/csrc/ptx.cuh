@@ -81,6 +81,24 @@ H3_DEV bool mbar_wait(uint32_t bar, uint32_t parity, int *status, bool honor_abo
   }
 }
 
+// The same for a whole converged warp, with one answer for all lanes.
+H3_DEV bool mbar_wait_warp(uint32_t bar, uint32_t parity, int *status, bool honor_abort = true) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, status, honor_abort));
+}
+// True in one lane of a converged warp. A warp that runs a loop of tcgen05
+// instructions converged, with only the instructions behind this, keeps their
+// operands in uniform registers.
+H3_DEV bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(p));
+  return p != 0;
+}
+
 // mbar_wait with a caller-given limit (for the bounded-wait self-test).
 H3_DEV bool mbar_wait_limit(uint32_t bar, uint32_t parity, int *status, long long limit_cycles) {
   const long long t0 = clock64();
@@ -471,6 +489,34 @@ H3_DEV void umma_commit_pair(uint32_t bar, uint16_t mask) {
       " [%0], %1;" ::"r"(bar),
       "h"(mask)
       : "memory");
+}
+
+// The scale copy and the FP4 products of a pair: each CTA's tensor memory gets
+// the scales from its own shared memory at the same offset; A's scales are those
+// of the CTA's 128 rows, W's those of all N columns, in both CTAs.
+H3_DEV void tmem_cp_sf_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
+               : "memory");
+}
+template <bool NV>
+H3_DEV void umma_fp4_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                          uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate) {
+  if constexpr (NV)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
 }
 
 // ---------------------------------------------------------------- misc
