@@ -1755,7 +1755,7 @@ h3dit_status run_linear_fp4(h3dit_ctx *ctx, int format, int epi, Fp4GemmParams &
   if (!fn) return ctx->fail(H3DIT_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   const int kernel_epi = epi == H3DIT_EPI_GELU && p.out_sf ? static_cast<int>(kEpiGeluFp4) : epi;
   const Fp4GemmPlan plan = fp4_gemm_plan(format, &p, ctx->num_sms);
-  Fp4GemmMaps t;
+  Fp4GemmMaps t{};
   auto encode = [&](CUtensorMap *m, CUtensorMapDataType type, const void *base, uint64_t row_bytes,
                     int elem, int rows, int box, int box_rows, CUtensorMapSwizzle swizzle) {
     const cuuint64_t dims[2] = {row_bytes / elem, static_cast<cuuint64_t>(rows)};
@@ -1781,6 +1781,12 @@ h3dit_status run_linear_fp4(h3dit_ctx *ctx, int format, int epi, Fp4GemmParams &
   if (r == CUDA_SUCCESS) r = codes(&t.b, w, p.n, plan.box_b);
   if (r == CUDA_SUCCESS && plan.pair) r = scales(&t.a_sf, p.a_sf, p.m, 1);
   if (r == CUDA_SUCCESS && plan.pair) r = scales(&t.b_sf, p.b_sf, p.n, 2);
+  if (r == CUDA_SUCCESS && plan.pair && kernel_epi != kEpiGeluFp4) {
+    const bool f32 = kernel_epi == kEpiGatedResidual;
+    r = encode(&t.out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+               p.out, static_cast<uint64_t>(p.n) * (f32 ? 4 : 2), f32 ? 4 : 2, p.m, 32, 32,
+               f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+  }
   if (r != CUDA_SUCCESS) return ctx->fail(H3DIT_ERR_CUDA, "tensor map encode failed (%d)", (int)r);
   Launch L(ctx, H3DIT_KERNEL_LINEAR_FP4, s);
   return ctx->cuda(launch_gemm_fp4(format, kernel_epi, t, p, plan, s), "FP4 gemm launch");

@@ -50,11 +50,27 @@ H3_DEV Alpha tensor_alpha(const float *ga, const float *gw) {
   return {x, y};
 }
 
-// v = alpha acc + bias for 32 columns, then the epilogue, straight to memory.
-template <int FMT, int EPI>
-H3_DEV void finish32(const Fp4GemmParams &p, const Alpha &al, float (&v)[32], int row, int col) {
+// 32 columns of a row's residual: all loads before the first use (out may be
+// resid, so the compiler would not move them past a store).
+struct Resid32 {
+  float4 x[8];
+};
+H3_DEV Resid32 load_resid(const Fp4GemmParams &p, int row, int col) {
+  Resid32 r;
+  const float4 *x =
+      reinterpret_cast<const float4 *>(p.resid + static_cast<size_t>(row) * p.n + col);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] *= al.a;
+  for (int q = 0; q < 8; ++q) r.x[q] = x[q];
+  return r;
+}
+
+// 32 accumulators of a row, as values: alpha acc + bias, then GELU, or the
+// gated addition to the residual.
+template <int EPI>
+H3_DEV void values32(const Fp4GemmParams &p, const Alpha &al, const uint32_t (&acc)[32], int col,
+                     const Resid32 &x, float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]) * al.a;
   if (al.b != 1.f) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) v[i] *= al.b;
@@ -70,44 +86,38 @@ H3_DEV void finish32(const Fp4GemmParams &p, const Alpha &al, float (&v)[32], in
       v[4 * q + 3] += bb.w;
     }
   }
-  const size_t at = static_cast<size_t>(row) * p.n + col;
   if constexpr (EPI == kEpiGatedResidual) {
     const float4 *g = reinterpret_cast<const float4 *>(p.gate + col);
-    const float4 *x = reinterpret_cast<const float4 *>(p.resid + at);
-    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      float4 a = x[q];
       const float4 gg = __ldg(g + q);
-      a.x = fmaf(gg.x, v[4 * q + 0], a.x);
-      a.y = fmaf(gg.y, v[4 * q + 1], a.y);
-      a.z = fmaf(gg.z, v[4 * q + 2], a.z);
-      a.w = fmaf(gg.w, v[4 * q + 3], a.w);
-      o[q] = a;
+      v[4 * q + 0] = fmaf(gg.x, v[4 * q + 0], x.x[q].x);
+      v[4 * q + 1] = fmaf(gg.y, v[4 * q + 1], x.x[q].y);
+      v[4 * q + 2] = fmaf(gg.z, v[4 * q + 2], x.x[q].z);
+      v[4 * q + 3] = fmaf(gg.w, v[4 * q + 3], x.x[q].w);
     }
-  } else {
-    if constexpr (EPI != kEpiStore) {
+  } else if constexpr (EPI != kEpiStore) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = gelu_f(v[i], p.gelu_tanh);
-    }
-    if constexpr (EPI == kEpiGeluFp4) {
-      const Fp4Tensor t = fp4_tensor(FMT == kFp4Nv ? p.out_scale : nullptr);
-      uint32_t q[4], sb[2];
-      fp4_quant32<FMT>(v, t, q, sb);
-      st_global_v4(static_cast<uint8_t *>(p.out) + at / 2, q[0], q[1], q[2], q[3]);
-      const int chunks = (p.n / Fp4<FMT>::BLOCK + 3) / 4;
-      const size_t o = mx_sf_offset(row, col / Fp4<FMT>::BLOCK, chunks);
-      if constexpr (FMT == kFp4Nv) {
-        *reinterpret_cast<uint16_t *>(p.out_sf + o) = static_cast<uint16_t>(sb[0] | (sb[1] << 8));
-      } else {
-        p.out_sf[o] = static_cast<uint8_t>(sb[0]);
-        // a row that ends with two of its last four scales: the others are 0
-        if (col + 32 == p.n && p.n % 128 == 64)
-          *reinterpret_cast<uint16_t *>(p.out_sf + o + 1) = 0;
-      }
-    } else {
-      store_bf16_row<32>(static_cast<uint16_t *>(p.out) + at, v);
-    }
+    for (int i = 0; i < 32; ++i) v[i] = gelu_f(v[i], p.gelu_tanh);
+  }
+}
+
+// 32 values of a row rounded to the operands' FP4 format.
+template <int FMT>
+H3_DEV void store_fp4(const Fp4GemmParams &p, const Fp4Tensor &t, const float (&v)[32], int row,
+                      int col) {
+  uint32_t q[4], sb[2];
+  fp4_quant32<FMT>(v, t, q, sb);
+  st_global_v4(static_cast<uint8_t *>(p.out) + (static_cast<size_t>(row) * p.n + col) / 2, q[0],
+               q[1], q[2], q[3]);
+  const int chunks = (p.n / Fp4<FMT>::BLOCK + 3) / 4;
+  uint8_t *sf = p.out_sf + mx_sf_offset(row, col / Fp4<FMT>::BLOCK, chunks);
+  if constexpr (FMT == kFp4Nv) {
+    *reinterpret_cast<uint16_t *>(sf) = static_cast<uint16_t>(sb[0] | (sb[1] << 8));
+  } else {
+    *sf = static_cast<uint8_t>(sb[0]);
+    // a row that ends with two of its last four scales: the others are 0
+    if (col + 32 == p.n && p.n % 128 == 64) *reinterpret_cast<uint16_t *>(sf + 1) = 0;
   }
 }
 
@@ -277,6 +287,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else {
     const int sub = warp & 3;
     const Alpha al = tensor_alpha(p.a_scale, p.b_scale);
+    Fp4Tensor to{};
+    if constexpr (EPI == kEpiGeluFp4) to = fp4_tensor(FMT == kFp4Nv ? p.out_scale : nullptr);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
@@ -290,12 +302,25 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int row = tm * BM + sub * 32 + lane;
 #pragma unroll 1
       for (int c = 0; c < BN && tn * BN + c < p.n; c += 32) {
+        const int col = tn * BN + c;
+        Resid32 x{};
+        if (EPI == kEpiGatedResidual && row < p.m) x = load_resid(p, row, col);
         uint32_t r[32];
         tmem_ld32(tbase + c, r);
         float v[32];
+        values32<EPI>(p, al, r, col, x, v);
+        if (row >= p.m) continue;
+        const size_t at = static_cast<size_t>(row) * p.n + col;
+        if constexpr (EPI == kEpiGatedResidual) {
+          float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-        if (row < p.m) finish32<FMT, EPI>(p, al, v, row, tn * BN + c);
+          for (int q = 0; q < 8; ++q)
+            o[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        } else if constexpr (EPI == kEpiGeluFp4) {
+          store_fp4<FMT>(p, to, v, row, col);
+        } else {
+          store_bf16_row<32>(static_cast<uint16_t *>(p.out) + at, v);
+        }
       }
       tc_fence_before();
       mbar_arrive(TEMPTY(acc));
@@ -324,28 +349,41 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const Fp4GemmPara
 }  // namespace one
 
 // ------------------------------------------------------- a pair of CTAs per tile
-// Output tiles of 256 x 192 on clusters of two CTAs (M256 N192 K64): each CTA
-// loads its own 128 rows of A and 96 of W's 192, so a byte from L2 feeds nearly
-// twice the MACs of a one-CTA tile. 2 x 192 columns of tensor memory hold two
-// accumulators, the other 128 the scales of SLOTS k-blocks: a slot is written
-// again once the MMAs that read it have completed (its k-block's EMPTY phase).
-// 192 columns start at 0 or 64 in a block of 128 scale rows; both blocks that
-// they touch are copied, and an odd tile's MMAs read them from column 2 on.
+// Output tiles of 256 x 256 on clusters of two CTAs (M256 N256 K64): each CTA
+// loads its own 128 rows of A and 128 of W's 256, so a byte from L2 feeds twice
+// the MACs of a one-CTA tile. (256 x 192, with two whole accumulators in tensor
+// memory, ran the products a fifth slower.)
+//
+// Tensor memory: the accumulators of successive tiles take columns 0..255 and
+// 160..415 in turn, the scales of SLOTS k-blocks columns 416..511. The two
+// share 96 columns: the epilogue reads those first, and with them in registers
+// lets the next tile's MMAs start; the rest of the epilogue runs beside them.
+// A scale slot is written again once the MMAs that read it have completed (its
+// k-block's EMPTY phase).
+//
+// The epilogue's rows go through shared memory (32 x 32 values per warp) and
+// leave by TMA stores.
 namespace pair {
-constexpr int BN = 192;
+constexpr int BN = 256;
 constexpr int PARTS = 2;  // epilogue warps per TMEM lane quarter
 constexpr int THREADS = 64 + 128 * PARTS;
 constexpr int STAGES = 5;
 constexpr int A_BYTES = BM * BKB, B_BYTES = BN / 2 * BKB;
+constexpr int OUT_BYTES = 4096;     // per epilogue warp: one fp32 or two bf16 boxes
+constexpr uint32_t ACC_STEP = 160;  // the second accumulator's first column
+constexpr uint32_t SF_COL0 = ACC_STEP + BN;
+constexpr int SHARED = (BN - ACC_STEP) / 32;  // chunks of 32 columns in both accumulators
 constexpr uint16_t kBothCtas = 0x3, kFirstCta = 0x1;
+static_assert(SHARED == 3 && BN / 32 == 8, "the epilogue's order of chunks");
 
 template <int FMT>
 struct Tile {
   static constexpr int SFA_BYTES = Kb<FMT>::CHUNKS * SF, SFB_BYTES = 2 * SFA_BYTES;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
-  static constexpr int NUM_BARS = 2 * STAGES + 4 + 1;
-  static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + NUM_BARS * 8 + 16;
-  static constexpr uint32_t SF_COL0 = 2 * BN;
+  static constexpr int NUM_BARS = 2 * STAGES + 3 + 1;
+  static constexpr int OUT_AT = STAGES * STAGE_BYTES;
+  static constexpr int BARS_AT = OUT_AT + 4 * PARTS * OUT_BYTES;
+  static constexpr int SMEM_BYTES = BARS_AT + 1024 + NUM_BARS * 8 + 16;
   static constexpr uint32_t SF_COLS = 12 * Kb<FMT>::CHUNKS;
   static constexpr int FIT = static_cast<int>((TMEM_COLS - SF_COL0) / SF_COLS);
   static constexpr int SLOTS = FIT < STAGES ? FIT : STAGES;
@@ -360,13 +398,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     gemm_fp4_pair(const __grid_constant__ CUtensorMap tma_a,
                   const __grid_constant__ CUtensorMap tma_b,
                   const __grid_constant__ CUtensorMap tma_sfa,
-                  const __grid_constant__ CUtensorMap tma_sfb, const Fp4GemmParams p) {
+                  const __grid_constant__ CUtensorMap tma_sfb,
+                  const __grid_constant__ CUtensorMap tma_out, const Fp4GemmParams p) {
   using T = Tile<FMT>;
   constexpr bool NV = FMT == kFp4Nv;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * T::STAGE_BYTES);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + T::BARS_AT);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + T::NUM_BARS);
   __shared__ int entry_status;
   __shared__ int loads_issued;
@@ -381,8 +420,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto FULL = [&](int s) { return bar0 + 8u * s; };
   auto EMPTY = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto TFULL = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
-  auto TEMPTY = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
-  const uint32_t DRAIN = bar0 + 8u * (2 * STAGES + 4);
+  const uint32_t TEMPTY = bar0 + 8u * (2 * STAGES + 2);  // the shared columns are in registers
+  const uint32_t DRAIN = bar0 + 8u * (2 * STAGES + 3);
 
   if (threadIdx.x == 0) {
     entry_status = *reinterpret_cast<const volatile int *>(p.status);
@@ -391,10 +430,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(FULL(s), 2);  // one arrival per producer of the pair
       mbar_init(EMPTY(s), 1);
     }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(TFULL(a), 1);
-      mbar_init(TEMPTY(a), 2 * 128 * PARTS);  // both CTAs' epilogue threads
-    }
+    for (int a = 0; a < 2; ++a) mbar_init(TFULL(a), 1);
+    mbar_init(TEMPTY, 2 * 128 * PARTS);  // both CTAs' epilogue threads
     mbar_init(DRAIN, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tma_a);
@@ -449,7 +486,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           tma_load_2d_pair(sa, &tma_a, kb * BKB, block_a * BM, full);
           tma_load_2d_pair(sa + A_BYTES, &tma_b, kb * BKB, row_b, full);
           tma_load_2d_pair(sa + A_BYTES + B_BYTES, &tma_sfa, sf_x, block_a, full);
-          tma_load_2d_pair(sa + A_BYTES + B_BYTES + T::SFA_BYTES, &tma_sfb, sf_x, tn * BN / 128,
+          tma_load_2d_pair(sa + A_BYTES + B_BYTES + T::SFA_BYTES, &tma_sfb, sf_x, tn * (BN / 128),
                            full);
           ++issued;
           if (++stage == STAGES) {
@@ -464,21 +501,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (leader) {
       int stage = 0, slot = 0;
       uint32_t phase = 0;
-      int acc = 0;
-      uint32_t acc_phase = 0;
-      int used = 0;  // slots written so far, up to SLOTS
+      uint32_t acc = 0, empty_phase = 1;  // the first tile waits for no epilogue
+      int used = 0;                       // slots written so far, up to SLOTS
       bool ok = true;
       for (int t = pair_id; t < num_tiles && ok; t += pairs) {
-        int tm, tn;
-        tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
-        const uint32_t odd = 2u * (tn & 1);
-        ok = mbar_wait_cluster(TEMPTY(acc), acc_phase ^ 1, p.status);
+        ok = mbar_wait_cluster(TEMPTY, empty_phase, p.status);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
+        const uint32_t d = tmem + acc * ACC_STEP;
         for (int kb = 0; kb < kblocks; ++kb) {
           ok = mbar_wait_warp(FULL(stage), phase, p.status);
           if (!ok) break;
@@ -492,7 +525,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t sa = sbase + stage * T::STAGE_BYTES;
           const uint64_t da = desc_sw128(sa, 16, 1024), db = desc_sw128(sa + A_BYTES, 16, 1024);
           const uint64_t dsf = desc_sf_copy(sa + A_BYTES + B_BYTES);
-          const uint32_t sfa = tmem + T::SF_COL0 + T::SF_COLS * slot;
+          const uint32_t sfa = tmem + SF_COL0 + T::SF_COLS * slot;
           const uint32_t sfb = sfa + 4 * Kb<FMT>::CHUNKS;
           const int groups = min(4, (p.k - kb * BK) / 64);
           if (elect_one()) {
@@ -509,7 +542,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (g >= groups) break;
               const int c = g / Kb<FMT>::PER_CHUNK, id = 2 * (g % Kb<FMT>::PER_CHUNK);
               umma_fp4_pair<NV>(d, da + 2 * g, db + 2 * g, idesc_fp4(2 * BM, BN, NV, id),
-                                sfa + 4 * c, sfb + 8 * c + odd, (kb | g) != 0 ? 1u : 0u);
+                                sfa + 4 * c, sfb + 8 * c, (kb | g) != 0 ? 1u : 0u);
             }
             umma_commit_pair(EMPTY(stage), kBothCtas);
           }
@@ -525,7 +558,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (elect_one()) umma_commit_pair(TFULL(acc), kBothCtas);
         __syncwarp();
         acc ^= 1;
-        if (acc == 0) acc_phase ^= 1;
+        empty_phase ^= 1;
       }
       // Every pair MMA (and the arrivals its commits make) completes before
       // either CTA may release TMEM or exit.
@@ -537,35 +570,97 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int sub = warp & 3;  // TMEM lane quarter this warp may access
     const int part = (warp - 2) >> 2;
     const Alpha al = tensor_alpha(p.a_scale, p.b_scale);
-    const uint32_t tempty_leader = map_to_cta(TEMPTY(0), 0);
-    int acc = 0;
-    uint32_t acc_phase = 0;
+    Fp4Tensor to{};
+    if constexpr (EPI == kEpiGeluFp4) to = fp4_tensor(FMT == kFp4Nv ? p.out_scale : nullptr);
+    const uint32_t tempty = map_to_cta(TEMPTY, 0);
+    const uint32_t out0 = sbase + T::OUT_AT + (warp - 2) * OUT_BYTES;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(sub * 32) << 16);
+    uint32_t acc = 0, full_phase = 0, flip = 0;
     for (int t = pair_id; t < num_tiles; t += pairs) {
       int tm, tn;
       tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
-      const bool ok = mbar_wait(TFULL(acc), acc_phase, p.status);
+      const int row0 = (2 * tm + static_cast<int>(rank)) * BM + sub * 32;
+      const int row = row0 + lane;
+      // this warp's four chunks of 32 columns, shared ones (two, or one) first
+      const int first = acc ? 0 : BN / 32 - SHARED, rest = acc ? SHARED : 0;
+      auto chunk = [&](int j) {
+        return part == 0 ? (j < 2 ? first + j : rest + j - 2) : (j < 1 ? first + 2 : rest + j + 1);
+      };
+      auto tbase = [&](int j) { return lanes + acc * ACC_STEP + 32 * chunk(j); };
+      auto resid = [&](int j) {
+        const int col = tn * BN + 32 * chunk(j);
+        Resid32 x{};
+        if (EPI == kEpiGatedResidual && row < p.m && col < p.n) x = load_resid(p, row, col);
+        return x;
+      };
+      auto finish = [&](int j, const uint32_t (&r)[32], const Resid32 &x) {
+        const int col = tn * BN + 32 * chunk(j);
+        if (col >= p.n || row0 >= p.m) return;  // the same for the whole warp
+        float v[32];
+        values32<EPI>(p, al, r, col, x, v);
+        if constexpr (EPI == kEpiGeluFp4) {
+          if (row < p.m) store_fp4<FMT>(p, to, v, row, col);
+        } else if constexpr (EPI == kEpiGatedResidual) {
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+          const uint32_t o = out0 + lane * 128;  // 128-byte swizzle: 16-byte unit q at q ^ (row % 8)
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            st_shared_v4(o + 16 * (q ^ (lane & 7)), __float_as_uint(v[4 * q]),
+                         __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                         __float_as_uint(v[4 * q + 3]));
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tma_out, col, row0, out0);
+            bulk_commit();
+          }
+        } else {
+          if (lane == 0) bulk_wait_read<1>();
+          __syncwarp();
+          const uint32_t box = out0 + flip * (OUT_BYTES / 2);
+          const uint32_t o = box + lane * 64;  // 64-byte swizzle: unit q at q ^ (row / 2 % 4)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            st_shared_v4(o + 16 * (q ^ ((lane >> 1) & 3)), pack_bf16x2(v[8 * q], v[8 * q + 1]),
+                         pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
+                         pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
+                         pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tma_out, col, row0, box);
+            bulk_commit();
+          }
+          flip ^= 1;
+        }
+      };
+      Resid32 xa = resid(0), xb;
+      const bool ok = mbar_wait(TFULL(acc), full_phase, p.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      const uint32_t tbase =
-          tmem + (static_cast<uint32_t>(sub * 32) << 16) + static_cast<uint32_t>(acc * BN);
-      const int row = (2 * tm + static_cast<int>(rank)) * BM + sub * 32 + lane;
-#pragma unroll 1
-      for (int c = 32 * part; c < BN && tn * BN + c < p.n; c += 32 * PARTS) {
-        uint32_t r[32];
-        tmem_ld32(tbase + c, r);
-        float v[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-        if (row < p.m) finish32<FMT, EPI>(p, al, v, row, tn * BN + c);
-      }
+      uint32_t ra[32], rb[32];
+      tmem_ld32(tbase(0), ra);
+      if (part == 0) tmem_ld32(tbase(1), rb);
       tc_fence_before();
       if (leader)
-        mbar_arrive(TEMPTY(acc));
+        mbar_arrive(TEMPTY);
       else
-        mbar_arrive_cluster(tempty_leader + 8u * acc);
+        mbar_arrive_cluster(tempty);
+      xb = resid(1);
+      finish(0, ra, xa);
+      if (part != 0) tmem_ld32(tbase(1), rb);
+      xa = resid(2);
+      finish(1, rb, xb);
+      tmem_ld32(tbase(2), ra);
+      xb = resid(3);
+      finish(2, ra, xa);
+      tmem_ld32(tbase(3), rb);
+      finish(3, rb, xb);
       acc ^= 1;
-      if (acc == 0) acc_phase ^= 1;
+      if (acc == 0) full_phase ^= 1;
     }
+    if (lane == 0) bulk_wait_all();
   }
 
   // Drain: every load either producer issued must land before its CTA exits.
@@ -610,7 +705,7 @@ cudaError_t launch(const Fp4GemmMaps &t, const Fp4GemmParams &p, int grid, cudaS
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm_fp4_pair<FMT, EPI>, t.a, t.b, t.a_sf, t.b_sf, p);
+  return cudaLaunchKernelEx(&cfg, gemm_fp4_pair<FMT, EPI>, t.a, t.b, t.a_sf, t.b_sf, t.out, p);
 }
 }  // namespace pair
 
