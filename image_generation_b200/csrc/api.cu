@@ -1784,8 +1784,8 @@ h3dit_status run_linear_fp4(h3dit_ctx *ctx, int format, int epi, Fp4GemmParams &
   if (r == CUDA_SUCCESS && plan.pair && kernel_epi != kEpiGeluFp4) {
     const bool f32 = kernel_epi == kEpiGatedResidual;
     r = encode(&t.out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-               p.out, static_cast<uint64_t>(p.n) * (f32 ? 4 : 2), f32 ? 4 : 2, p.m, 32, 32,
-               f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+               p.out, static_cast<uint64_t>(p.n) * (f32 ? 4 : 2), f32 ? 4 : 2, p.m, f32 ? 32 : 64, 32,
+               CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (r != CUDA_SUCCESS) return ctx->fail(H3DIT_ERR_CUDA, "tensor map encode failed (%d)", (int)r);
   Launch L(ctx, H3DIT_KERNEL_LINEAR_FP4, s);

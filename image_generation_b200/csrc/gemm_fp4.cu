@@ -97,8 +97,14 @@ H3_DEV void values32(const Fp4GemmParams &p, const Alpha &al, const uint32_t (&a
       v[4 * q + 3] = fmaf(gg.w, v[4 * q + 3], x.x[q].w);
     }
   } else if constexpr (EPI != kEpiStore) {
+    // one branch for the 32, not one each
+    if (p.gelu_tanh) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = gelu_f(v[i], p.gelu_tanh);
+      for (int i = 0; i < 32; ++i) v[i] = gelu_f(v[i], 1);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = gelu_f(v[i], 0);
+    }
   }
 }
 
@@ -355,26 +361,25 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const Fp4GemmPara
 // memory, ran the products a fifth slower.)
 //
 // Tensor memory: the accumulators of successive tiles take columns 0..255 and
-// 160..415 in turn, the scales of SLOTS k-blocks columns 416..511. The two
-// share 96 columns: the epilogue reads those first, and with them in registers
+// 128..383 in turn, the scales of SLOTS k-blocks columns 384..511. The two
+// share 128 columns: the epilogue reads those first, and with them in registers
 // lets the next tile's MMAs start; the rest of the epilogue runs beside them.
 // A scale slot is written again once the MMAs that read it have completed (its
 // k-block's EMPTY phase).
 //
-// The epilogue's rows go through shared memory (32 x 32 values per warp) and
-// leave by TMA stores.
+// The epilogue's rows go through shared memory (boxes of 32 rows x 128 bytes per
+// warp) and leave by TMA stores.
 namespace pair {
 constexpr int BN = 256;
 constexpr int PARTS = 2;  // epilogue warps per TMEM lane quarter
 constexpr int THREADS = 64 + 128 * PARTS;
 constexpr int STAGES = 5;
 constexpr int A_BYTES = BM * BKB, B_BYTES = BN / 2 * BKB;
-constexpr int OUT_BYTES = 4096;     // per epilogue warp: one fp32 or two bf16 boxes
-constexpr uint32_t ACC_STEP = 160;  // the second accumulator's first column
+constexpr int OUT_BYTES = 4096;     // per epilogue warp: a box of 32 rows x 128 bytes
+constexpr uint32_t ACC_STEP = 128;  // the second accumulator's first column
 constexpr uint32_t SF_COL0 = ACC_STEP + BN;
-constexpr int SHARED = (BN - ACC_STEP) / 32;  // chunks of 32 columns in both accumulators
 constexpr uint16_t kBothCtas = 0x3, kFirstCta = 0x1;
-static_assert(SHARED == 3 && BN / 32 == 8, "the epilogue's order of chunks");
+static_assert(BN == 2 * ACC_STEP && BN == 2 * 64 * PARTS, "the epilogue's order of columns");
 
 template <int FMT>
 struct Tile {
@@ -431,7 +436,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(EMPTY(s), 1);
     }
     for (int a = 0; a < 2; ++a) mbar_init(TFULL(a), 1);
-    mbar_init(TEMPTY, 2 * 128 * PARTS);  // both CTAs' epilogue threads
+    mbar_init(TEMPTY, 2 * 4 * PARTS);  // both CTAs' epilogue warps
     mbar_init(DRAIN, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tma_a);
@@ -459,44 +464,43 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int pairs = gridDim.x >> 1;
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t full_leader = map_to_cta(FULL(0), 0);
-      int stage = 0;
-      uint32_t phase = 0;
-      int issued = 0;
-      bool ok = true;
-      for (int t = pair_id; t < num_tiles && ok; t += pairs) {
-        int tm, tn;
-        tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
-        const int block_a = 2 * tm + static_cast<int>(rank);
-        const int row_b = tn * BN + static_cast<int>(rank) * (BN / 2);
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait(EMPTY(stage), phase ^ 1, p.status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t full = full_leader + 8u * stage;
+    const uint32_t full_leader = map_to_cta(FULL(0), 0);
+    int stage = 0;
+    uint32_t phase = 0;
+    int issued = 0;
+    bool ok = true;
+    for (int t = pair_id; t < num_tiles && ok; t += pairs) {
+      int tm, tn;
+      tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
+      const int block_a = 2 * tm + static_cast<int>(rank);
+      const int row_b = tn * BN + static_cast<int>(rank) * (BN / 2);
+      for (int kb = 0; kb < kblocks; ++kb) {
+        ok = mbar_wait_warp(EMPTY(stage), phase ^ 1, p.status);
+        if (!ok) break;
+        const uint32_t full = full_leader + 8u * stage;
+        const uint32_t sa = sbase + stage * T::STAGE_BYTES;
+        if (elect_one()) {
           // boxes count whole, also where they read past a matrix
           if (leader)
             mbar_arrive_expect_tx(FULL(stage), T::STAGE_BYTES);
           else
             mbar_arrive_expect_tx_cluster(full, T::STAGE_BYTES);
-          const uint32_t sa = sbase + stage * T::STAGE_BYTES;
           const int sf_x = kb * (T::SFA_BYTES / 8);  // 8-byte elements
           tma_load_2d_pair(sa, &tma_a, kb * BKB, block_a * BM, full);
           tma_load_2d_pair(sa + A_BYTES, &tma_b, kb * BKB, row_b, full);
           tma_load_2d_pair(sa + A_BYTES + B_BYTES, &tma_sfa, sf_x, block_a, full);
           tma_load_2d_pair(sa + A_BYTES + B_BYTES + T::SFA_BYTES, &tma_sfb, sf_x, tn * (BN / 128),
                            full);
-          ++issued;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      loads_issued = issued;
     }
+    if (lane == 0) loads_issued = issued;
   } else if (warp == 1) {
     if (leader) {
       int stage = 0, slot = 0;
@@ -513,14 +517,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         const uint32_t d = tmem + acc * ACC_STEP;
         for (int kb = 0; kb < kblocks; ++kb) {
-          ok = mbar_wait_warp(FULL(stage), phase, p.status);
-          if (!ok) break;
           if (T::SLOTS < STAGES && used == T::SLOTS) {
             const bool wrapped = stage < T::SLOTS;  // the k-block SLOTS before this one
             ok = mbar_wait_warp(EMPTY(wrapped ? stage - T::SLOTS + STAGES : stage - T::SLOTS),
                                 wrapped ? phase ^ 1 : phase, p.status);
             if (!ok) break;
           }
+          ok = mbar_wait_warp(FULL(stage), phase, p.status);
+          if (!ok) break;
           tc_fence_after();
           const uint32_t sa = sbase + stage * T::STAGE_BYTES;
           const uint64_t da = desc_sw128(sa, 16, 1024), db = desc_sw128(sa + A_BYTES, 16, 1024);
@@ -575,16 +579,16 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tempty = map_to_cta(TEMPTY, 0);
     const uint32_t out0 = sbase + T::OUT_AT + (warp - 2) * OUT_BYTES;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(sub * 32) << 16);
-    uint32_t acc = 0, full_phase = 0, flip = 0;
+    uint32_t acc = 0, full_phase = 0;
     for (int t = pair_id; t < num_tiles; t += pairs) {
       int tm, tn;
       tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
       const int row0 = (2 * tm + static_cast<int>(rank)) * BM + sub * 32;
       const int row = row0 + lane;
-      // this warp's four chunks of 32 columns, shared ones (two, or one) first
-      const int first = acc ? 0 : BN / 32 - SHARED, rest = acc ? SHARED : 0;
+      // this warp's 64 of the shared columns, then 64 of the others, by 32
       auto chunk = [&](int j) {
-        return part == 0 ? (j < 2 ? first + j : rest + j - 2) : (j < 1 ? first + 2 : rest + j + 1);
+        const bool high = (acc != 0) != (j < 2);  // the accumulator's columns 128..255
+        return (high ? 4 : 0) + 2 * part + (j & 1);
       };
       auto tbase = [&](int j) { return lanes + acc * ACC_STEP + 32 * chunk(j); };
       auto resid = [&](int j) {
@@ -616,23 +620,27 @@ __global__ void __launch_bounds__(THREADS, 1)
             bulk_commit();
           }
         } else {
-          if (lane == 0) bulk_wait_read<1>();
-          __syncwarp();
-          const uint32_t box = out0 + flip * (OUT_BYTES / 2);
-          const uint32_t o = box + lane * 64;  // 64-byte swizzle: unit q at q ^ (row / 2 % 4)
+          if ((j & 1) == 0) {
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+          }
+          const uint32_t o = out0 + lane * 128;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            st_shared_v4(o + 16 * (q ^ ((lane >> 1) & 3)), pack_bf16x2(v[8 * q], v[8 * q + 1]),
+            st_shared_v4(o + 16 * ((q + 4 * (j & 1)) ^ (lane & 7)),
+                         pack_bf16x2(v[8 * q], v[8 * q + 1]),
                          pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
                          pack_bf16x2(v[8 * q + 4], v[8 * q + 5]),
                          pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&tma_out, col, row0, box);
-            bulk_commit();
+          // the box is whole with its second half, or where the matrix ends
+          if ((j & 1) == 1 || col + 32 >= p.n) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tma_out, col & ~63, row0, out0);
+              bulk_commit();
+            }
           }
-          flip ^= 1;
         }
       };
       Resid32 xa = resid(0), xb;
@@ -641,15 +649,17 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_after();
       uint32_t ra[32], rb[32];
       tmem_ld32(tbase(0), ra);
-      if (part == 0) tmem_ld32(tbase(1), rb);
+      tmem_ld32(tbase(1), rb);
       tc_fence_before();
-      if (leader)
-        mbar_arrive(TEMPTY);
-      else
-        mbar_arrive_cluster(tempty);
+      __syncwarp();
+      if (lane == 0) {
+        if (leader)
+          mbar_arrive(TEMPTY);
+        else
+          mbar_arrive_cluster(tempty);
+      }
       xb = resid(1);
       finish(0, ra, xa);
-      if (part != 0) tmem_ld32(tbase(1), rb);
       xa = resid(2);
       finish(1, rb, xb);
       tmem_ld32(tbase(2), ra);

@@ -248,8 +248,8 @@ struct Fp4GemmPlan {
 Fp4GemmPlan fp4_gemm_plan(int fmt, Fp4GemmParams *p, int num_sms);
 // Codes as rows of bytes in boxes of 128 bytes; for a pair also the scale
 // arrays, as rows of 8-byte elements (a row: the scale blocks of 128 rows), and
-// the output in boxes of 32 x 32 (bf16 in 64-byte, fp32 in 128-byte swizzle;
-// unused where the output is FP4).
+// the output in boxes of 32 rows x 128 bytes, 128-byte swizzle (unused where the
+// output is FP4).
 struct Fp4GemmMaps {
   CUtensorMap a, b, a_sf, b_sf, out;
 };
