@@ -64,6 +64,31 @@ H3_DEV Resid32 load_resid(const Fp4GemmParams &p, int row, int col) {
   return r;
 }
 
+// erf GELU of two values, x Phi(x) = max(x, 0) - |x| q with q = erfc(|x| / sqrt 2) / 2
+// by Abramowitz & Stegun, Handbook of Mathematical Functions, 7.1.26 (|error| of
+// erf <= 1.5e-7): q = t (b1 + ... + b5 t^4) e^(-x^2 / 2), t = 1 / (1 + p |x| / sqrt 2).
+// In packed fp32 pairs: one value at a time, the epilogue of a product
+// 16896 x 14336 x 5376 took 97 of its 514 us.
+H3_DEV void gelu2(float &a, float &b) {
+  auto c2 = [](float c) { return f2_pack(c, c); };
+  const uint64_t x = f2_pack(a, b), ax = f2_pack(fabsf(a), fabsf(b));
+  float d0, d1, t0, t1, e0, e1;
+  f2_unpack(f2_fma(ax, c2(0.3275911f * 0.70710678118654752f), c2(1.f)), d0, d1);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(d0));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t1) : "f"(d1));
+  f2_unpack(f2_mul(f2_mul(x, c2(-0.5f * 1.4426950408889634f)), x), e0, e1);
+  const uint64_t t = f2_pack(t0, t1), e = f2_pack(ex2_approx(e0), ex2_approx(e1));
+  uint64_t q = f2_fma(c2(0.5f * 1.061405429f), t, c2(0.5f * -1.453152027f));
+  q = f2_fma(q, t, c2(0.5f * 1.421413741f));
+  q = f2_fma(q, t, c2(0.5f * -0.284496736f));
+  q = f2_fma(q, t, c2(0.5f * 0.254829592f));
+  q = f2_mul(f2_mul(q, t), f2_mul(e, ax));
+  float q0, q1;
+  f2_unpack(q, q0, q1);
+  a = fmaxf(a, 0.f) - q0;
+  b = fmaxf(b, 0.f) - q1;
+}
+
 // 32 accumulators of a row, as values: alpha acc + bias, then GELU, or the
 // gated addition to the residual.
 template <int EPI>
@@ -103,7 +128,7 @@ H3_DEV void values32(const Fp4GemmParams &p, const Alpha &al, const uint32_t (&a
       for (int i = 0; i < 32; ++i) v[i] = gelu_f(v[i], 1);
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = gelu_f(v[i], 0);
+      for (int i = 0; i < 32; i += 2) gelu2(v[i], v[i + 1]);
     }
   }
 }
@@ -360,40 +385,37 @@ cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const Fp4GemmPara
 // the MACs of a one-CTA tile. (256 x 192, with two whole accumulators in tensor
 // memory, ran the products a fifth slower.)
 //
-// Tensor memory: the accumulators of successive tiles take columns 0..255 and
-// 128..383 in turn, the scales of SLOTS k-blocks columns 384..511. The two
-// share 128 columns: the epilogue reads those first, and with them in registers
-// lets the next tile's MMAs start; the rest of the epilogue runs beside them.
-// A scale slot is written again once the MMAs that read it have completed (its
-// k-block's EMPTY phase).
+// Tensor memory: one accumulator in columns 0..255, and in 256..511 the scales of
+// every stage. The epilogue first reads the whole accumulator into registers (128
+// columns of a row per thread) and then lets the next tile's MMAs start; its
+// arithmetic and stores run beside them. Overlapping the accumulators of
+// successive tiles instead, for a shorter pause between them, leaves the scales of
+// NVFP4 two k-blocks of columns; waiting for those cost more than the pause.
 //
 // The epilogue's rows go through shared memory (boxes of 32 rows x 128 bytes per
 // warp) and leave by TMA stores.
 namespace pair {
 constexpr int BN = 256;
-constexpr int PARTS = 2;  // epilogue warps per TMEM lane quarter
+constexpr int PARTS = 2;         // epilogue warps per TMEM lane quarter
 constexpr int THREADS = 64 + 128 * PARTS;
 constexpr int STAGES = 5;
 constexpr int A_BYTES = BM * BKB, B_BYTES = BN / 2 * BKB;
-constexpr int OUT_BYTES = 4096;     // per epilogue warp: a box of 32 rows x 128 bytes
-constexpr uint32_t ACC_STEP = 128;  // the second accumulator's first column
-constexpr uint32_t SF_COL0 = ACC_STEP + BN;
+constexpr int OUT_BYTES = 4096;  // per epilogue warp: a box of 32 rows x 128 bytes
+constexpr uint32_t SF_COL0 = BN;
 constexpr uint16_t kBothCtas = 0x3, kFirstCta = 0x1;
-static_assert(BN == 2 * ACC_STEP && BN == 2 * 64 * PARTS, "the epilogue's order of columns");
+static_assert(BN == 2 * 64 * PARTS, "two boxes of 64 columns per epilogue warp and tile");
 
 template <int FMT>
 struct Tile {
   static constexpr int SFA_BYTES = Kb<FMT>::CHUNKS * SF, SFB_BYTES = 2 * SFA_BYTES;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
-  static constexpr int NUM_BARS = 2 * STAGES + 3 + 1;
+  static constexpr int NUM_BARS = 2 * STAGES + 3;
   static constexpr int OUT_AT = STAGES * STAGE_BYTES;
   static constexpr int BARS_AT = OUT_AT + 4 * PARTS * OUT_BYTES;
   static constexpr int SMEM_BYTES = BARS_AT + 1024 + NUM_BARS * 8 + 16;
   static constexpr uint32_t SF_COLS = 12 * Kb<FMT>::CHUNKS;
-  static constexpr int FIT = static_cast<int>((TMEM_COLS - SF_COL0) / SF_COLS);
-  static constexpr int SLOTS = FIT < STAGES ? FIT : STAGES;
 };
-static_assert(Tile<kFp4Nv>::SLOTS >= 2 && Tile<kFp4Mx>::SLOTS >= 2, "TMEM budget");
+static_assert(SF_COL0 + STAGES * Tile<kFp4Nv>::SF_COLS <= TMEM_COLS, "TMEM budget");
 static_assert(Tile<kFp4Nv>::STAGE_BYTES % 1024 == 0 && Tile<kFp4Mx>::STAGE_BYTES % 1024 == 0,
               "stages start on swizzle atoms");
 static_assert(Tile<kFp4Nv>::SMEM_BYTES <= 227 * 1024, "shared memory budget");
@@ -424,9 +446,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t bar0 = smem_u32(bars);
   auto FULL = [&](int s) { return bar0 + 8u * s; };
   auto EMPTY = [&](int s) { return bar0 + 8u * (STAGES + s); };
-  auto TFULL = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
-  const uint32_t TEMPTY = bar0 + 8u * (2 * STAGES + 2);  // the shared columns are in registers
-  const uint32_t DRAIN = bar0 + 8u * (2 * STAGES + 3);
+  const uint32_t TFULL = bar0 + 8u * (2 * STAGES);       // a tile is accumulated
+  const uint32_t TEMPTY = bar0 + 8u * (2 * STAGES + 1);  // it is in registers
+  const uint32_t DRAIN = bar0 + 8u * (2 * STAGES + 2);
 
   if (threadIdx.x == 0) {
     entry_status = *reinterpret_cast<const volatile int *>(p.status);
@@ -435,7 +457,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(FULL(s), 2);  // one arrival per producer of the pair
       mbar_init(EMPTY(s), 1);
     }
-    for (int a = 0; a < 2; ++a) mbar_init(TFULL(a), 1);
+    mbar_init(TFULL, 1);
     mbar_init(TEMPTY, 2 * 4 * PARTS);  // both CTAs' epilogue warps
     mbar_init(DRAIN, 1);
     fence_mbar_init();
@@ -503,10 +525,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (lane == 0) loads_issued = issued;
   } else if (warp == 1) {
     if (leader) {
-      int stage = 0, slot = 0;
+      int stage = 0;
       uint32_t phase = 0;
-      uint32_t acc = 0, empty_phase = 1;  // the first tile waits for no epilogue
-      int used = 0;                       // slots written so far, up to SLOTS
+      uint32_t empty_phase = 1;  // the first tile waits for no epilogue
       bool ok = true;
       for (int t = pair_id; t < num_tiles && ok; t += pairs) {
         ok = mbar_wait_cluster(TEMPTY, empty_phase, p.status);
@@ -515,21 +536,14 @@ __global__ void __launch_bounds__(THREADS, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + acc * ACC_STEP;
         for (int kb = 0; kb < kblocks; ++kb) {
-          if (T::SLOTS < STAGES && used == T::SLOTS) {
-            const bool wrapped = stage < T::SLOTS;  // the k-block SLOTS before this one
-            ok = mbar_wait_warp(EMPTY(wrapped ? stage - T::SLOTS + STAGES : stage - T::SLOTS),
-                                wrapped ? phase ^ 1 : phase, p.status);
-            if (!ok) break;
-          }
           ok = mbar_wait_warp(FULL(stage), phase, p.status);
           if (!ok) break;
           tc_fence_after();
           const uint32_t sa = sbase + stage * T::STAGE_BYTES;
           const uint64_t da = desc_sw128(sa, 16, 1024), db = desc_sw128(sa + A_BYTES, 16, 1024);
           const uint64_t dsf = desc_sf_copy(sa + A_BYTES + B_BYTES);
-          const uint32_t sfa = tmem + SF_COL0 + T::SF_COLS * slot;
+          const uint32_t sfa = tmem + SF_COL0 + T::SF_COLS * stage;
           const uint32_t sfb = sfa + 4 * Kb<FMT>::CHUNKS;
           const int groups = min(4, (p.k - kb * BK) / 64);
           if (elect_one()) {
@@ -545,23 +559,20 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int g = 0; g < 4; ++g) {
               if (g >= groups) break;
               const int c = g / Kb<FMT>::PER_CHUNK, id = 2 * (g % Kb<FMT>::PER_CHUNK);
-              umma_fp4_pair<NV>(d, da + 2 * g, db + 2 * g, idesc_fp4(2 * BM, BN, NV, id),
+              umma_fp4_pair<NV>(tmem, da + 2 * g, db + 2 * g, idesc_fp4(2 * BM, BN, NV, id),
                                 sfa + 4 * c, sfb + 8 * c, (kb | g) != 0 ? 1u : 0u);
             }
             umma_commit_pair(EMPTY(stage), kBothCtas);
           }
           __syncwarp();
-          if (used < T::SLOTS) ++used;
-          if (++slot == T::SLOTS) slot = 0;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        if (elect_one()) umma_commit_pair(TFULL(acc), kBothCtas);
+        if (elect_one()) umma_commit_pair(TFULL, kBothCtas);
         __syncwarp();
-        acc ^= 1;
         empty_phase ^= 1;
       }
       // Every pair MMA (and the arrivals its commits make) completes before
@@ -579,27 +590,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tempty = map_to_cta(TEMPTY, 0);
     const uint32_t out0 = sbase + T::OUT_AT + (warp - 2) * OUT_BYTES;
     const uint32_t lanes = tmem + (static_cast<uint32_t>(sub * 32) << 16);
-    uint32_t acc = 0, full_phase = 0;
+    uint32_t full_phase = 0;
     for (int t = pair_id; t < num_tiles; t += pairs) {
       int tm, tn;
       tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
       const int row0 = (2 * tm + static_cast<int>(rank)) * BM + sub * 32;
       const int row = row0 + lane;
-      // this warp's 64 of the shared columns, then 64 of the others, by 32
-      auto chunk = [&](int j) {
-        const bool high = (acc != 0) != (j < 2);  // the accumulator's columns 128..255
-        return (high ? 4 : 0) + 2 * part + (j & 1);
-      };
-      auto tbase = [&](int j) { return lanes + acc * ACC_STEP + 32 * chunk(j); };
-      auto resid = [&](int j) {
-        const int col = tn * BN + 32 * chunk(j);
-        Resid32 x{};
-        if (EPI == kEpiGatedResidual && row < p.m && col < p.n) x = load_resid(p, row, col);
-        return x;
-      };
-      auto finish = [&](int j, const uint32_t (&r)[32], const Resid32 &x) {
-        const int col = tn * BN + 32 * chunk(j);
+      const int col0 = tn * BN + 128 * part;  // this warp's 128 columns, by 32
+      if (EPI == kEpiGatedResidual && row < p.m) {
+        // the residual on its way to L2 while the tile is accumulated
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (col0 + 32 * j < p.n)
+            prefetch_l2(p.resid + static_cast<size_t>(row) * p.n + col0 + 32 * j);
+      }
+      auto finish = [&](int j, const uint32_t (&r)[32]) {
+        const int col = col0 + 32 * j;
         if (col >= p.n || row0 >= p.m) return;  // the same for the whole warp
+        Resid32 x{};
+        if (EPI == kEpiGatedResidual && row < p.m) x = load_resid(p, row, col);
         float v[32];
         values32<EPI>(p, al, r, col, x, v);
         if constexpr (EPI == kEpiGeluFp4) {
@@ -643,13 +652,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       };
-      Resid32 xa = resid(0), xb;
-      const bool ok = mbar_wait(TFULL(acc), full_phase, p.status);
+      const bool ok = mbar_wait(TFULL, full_phase, p.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      uint32_t ra[32], rb[32];
-      tmem_ld32(tbase(0), ra);
-      tmem_ld32(tbase(1), rb);
+      uint32_t r[4][32];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) tmem_ld32_async(lanes + 128 * part + 32 * j, r[j]);
+      tmem_wait_ld(r[0], r[1], r[2], r[3]);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -658,17 +667,9 @@ __global__ void __launch_bounds__(THREADS, 1)
         else
           mbar_arrive_cluster(tempty);
       }
-      xb = resid(1);
-      finish(0, ra, xa);
-      xa = resid(2);
-      finish(1, rb, xb);
-      tmem_ld32(tbase(2), ra);
-      xb = resid(3);
-      finish(2, ra, xa);
-      tmem_ld32(tbase(3), rb);
-      finish(3, rb, xb);
-      acc ^= 1;
-      if (acc == 0) full_phase ^= 1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) finish(j, r[j]);
+      full_phase ^= 1;
     }
     if (lane == 0) bulk_wait_all();
   }
