@@ -597,26 +597,36 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int row0 = (2 * tm + static_cast<int>(rank)) * BM + sub * 32;
       const int row = row0 + lane;
       const int col0 = tn * BN + 128 * part;  // this warp's 128 columns, by 32
-      if (EPI == kEpiGatedResidual && row < p.m) {
-        // the residual on its way to L2 while the tile is accumulated
+      // 32 columns of the warp's rows of the residual into its box, whole lines at
+      // a time (a thread's own row at a time, the warps' lines did not fit into L1)
+      auto fetch = [&](int j) {
+        if (EPI != kEpiGatedResidual || col0 + 32 * j >= p.n || row0 >= p.m) return;
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (col0 + 32 * j < p.n)
-            prefetch_l2(p.resid + static_cast<size_t>(row) * p.n + col0 + 32 * j);
-      }
+        for (int i = 0; i < 8; ++i) {
+          const int r = 4 * i + (lane >> 3), u = lane & 7;
+          if (row0 + r < p.m)
+            cp_async16(out0 + r * 128 + 16 * (u ^ (r & 7)),
+                       p.resid + static_cast<size_t>(row0 + r) * p.n + col0 + 32 * j + 4 * u);
+        }
+      };
       auto finish = [&](int j, const uint32_t (&r)[32]) {
         const int col = col0 + 32 * j;
         if (col >= p.n || row0 >= p.m) return;  // the same for the whole warp
         Resid32 x{};
-        if (EPI == kEpiGatedResidual && row < p.m) x = load_resid(p, row, col);
+        const uint32_t o = out0 + lane * 128;  // 128-byte swizzle: 16-byte unit q at q ^ (row % 8)
+        if constexpr (EPI == kEpiGatedResidual) {
+          cp_async_wait_all();
+          __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) x.x[q] = ld_shared_v4(o + 16 * (q ^ (lane & 7)));
+        }
         float v[32];
         values32<EPI>(p, al, r, col, x, v);
         if constexpr (EPI == kEpiGeluFp4) {
           if (row < p.m) store_fp4<FMT>(p, to, v, row, col);
         } else if constexpr (EPI == kEpiGatedResidual) {
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
-          const uint32_t o = out0 + lane * 128;  // 128-byte swizzle: 16-byte unit q at q ^ (row % 8)
 #pragma unroll
           for (int q = 0; q < 8; ++q)
             st_shared_v4(o + 16 * (q ^ (lane & 7)), __float_as_uint(v[4 * q]),
@@ -628,12 +638,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             tma_store_2d(&tma_out, col, row0, out0);
             bulk_commit();
           }
+          if (j < 3) fetch(j + 1);
         } else {
           if ((j & 1) == 0) {
             if (lane == 0) bulk_wait_read<0>();
             __syncwarp();
           }
-          const uint32_t o = out0 + lane * 128;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             st_shared_v4(o + 16 * ((q + 4 * (j & 1)) ^ (lane & 7)),
@@ -652,6 +662,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
         }
       };
+      fetch(0);
       const bool ok = mbar_wait(TFULL, full_phase, p.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
@@ -671,6 +682,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int j = 0; j < 4; ++j) finish(j, r[j]);
       full_phase ^= 1;
     }
+    cp_async_wait_all();
     if (lane == 0) bulk_wait_all();
   }
 
