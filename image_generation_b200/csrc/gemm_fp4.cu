@@ -7,12 +7,15 @@
 //   GATED_RESIDUAL   out fp32 = resid + gate * v
 // with v = alpha acc + bias.
 //
-// Structure (one CTA per SM, persistent over 128 x 128 output tiles):
-//   warp 0      TMA producer: A and W boxes of 128 rows x 128 bytes (256 k, in
-//               128-byte swizzle) and that k-block's scale blocks into a ring;
-//   warp 1      MMA issuer: tcgen05.cp of the scale blocks into tensor memory,
-//               then one MMA (M128 N128 K64) per 64 k;
-//   warps 2..5  epilogue: one row of the tile per thread.
+// Two kernels: 256 x 256 tiles on pairs of CTAs, persistent, for products that
+// fill the SMs with them; 128 x 128 tiles with k split over a cluster for the
+// rest. In both one warp loads (128 bytes = 256 k of each row per k-block, in
+// 128-byte swizzle, and that k-block's scale blocks, into a ring of stages), one
+// warp copies the scales into tensor memory (tcgen05.cp) and issues the MMAs, one
+// per 64 k, and the others run the epilogue. The loading and the issuing warp
+// stay converged and elect a lane around their instructions: from a single
+// lane's branch, the operands' way into uniform registers took twice the MMAs' time.
+//
 // k is a multiple of 64: a last k-block with fewer than four groups of 64 reads
 // zeros past the row (TMA fill) and issues only the MMAs whose k exist, so the
 // padding of the scale blocks is never multiplied.
@@ -50,20 +53,6 @@ H3_DEV Alpha tensor_alpha(const float *ga, const float *gw) {
   return {x, y};
 }
 
-// 32 columns of a row's residual: all loads before the first use (out may be
-// resid, so the compiler would not move them past a store).
-struct Resid32 {
-  float4 x[8];
-};
-H3_DEV Resid32 load_resid(const Fp4GemmParams &p, int row, int col) {
-  Resid32 r;
-  const float4 *x =
-      reinterpret_cast<const float4 *>(p.resid + static_cast<size_t>(row) * p.n + col);
-#pragma unroll
-  for (int q = 0; q < 8; ++q) r.x[q] = x[q];
-  return r;
-}
-
 // erf GELU of two values, x Phi(x) = max(x, 0) - |x| q with q = erfc(|x| / sqrt 2) / 2
 // by Abramowitz & Stegun, Handbook of Mathematical Functions, 7.1.26 (|error| of
 // erf <= 1.5e-7): q = t (b1 + ... + b5 t^4) e^(-x^2 / 2), t = 1 / (1 + p |x| / sqrt 2).
@@ -90,10 +79,10 @@ H3_DEV void gelu2(float &a, float &b) {
 }
 
 // 32 accumulators of a row, as values: alpha acc + bias, then GELU, or the
-// gated addition to the residual.
-template <int EPI>
+// gated addition to the residual (resid(q): columns 4 q .. 4 q + 3 of it).
+template <int EPI, typename Resid>
 H3_DEV void values32(const Fp4GemmParams &p, const Alpha &al, const uint32_t (&acc)[32], int col,
-                     const Resid32 &x, float (&v)[32]) {
+                     Resid &&resid, float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]) * al.a;
   if (al.b != 1.f) {
@@ -115,11 +104,11 @@ H3_DEV void values32(const Fp4GemmParams &p, const Alpha &al, const uint32_t (&a
     const float4 *g = reinterpret_cast<const float4 *>(p.gate + col);
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      const float4 gg = __ldg(g + q);
-      v[4 * q + 0] = fmaf(gg.x, v[4 * q + 0], x.x[q].x);
-      v[4 * q + 1] = fmaf(gg.y, v[4 * q + 1], x.x[q].y);
-      v[4 * q + 2] = fmaf(gg.z, v[4 * q + 2], x.x[q].z);
-      v[4 * q + 3] = fmaf(gg.w, v[4 * q + 3], x.x[q].w);
+      const float4 gg = __ldg(g + q), x = resid(q);
+      v[4 * q + 0] = fmaf(gg.x, v[4 * q + 0], x.x);
+      v[4 * q + 1] = fmaf(gg.y, v[4 * q + 1], x.y);
+      v[4 * q + 2] = fmaf(gg.z, v[4 * q + 2], x.z);
+      v[4 * q + 3] = fmaf(gg.w, v[4 * q + 3], x.w);
     }
   } else if constexpr (EPI != kEpiStore) {
     // one branch for the 32, not one each
@@ -152,30 +141,59 @@ H3_DEV void store_fp4(const Fp4GemmParams &p, const Fp4Tensor &t, const float (&
   }
 }
 
-// ------------------------------------------------------------ one CTA per tile
-namespace one {
+// ---------------------------------------------------------- few tiles: split k
+// Output tiles of 128 x 128, one per CTA or per cluster of up to eight CTAs that
+// share its k-blocks: for few rows (where reading W bounds the call) and for
+// products with too few 256 x 256 tiles to fill the SMs. Two CTAs fit on an SM, so
+// one's epilogue runs beside the other's loads.
+//   warp 0 TMA and bulk loads, warp 1 MMAs (M128 N128 K64), warps 2..5 epilogue.
+// In a cluster each CTA leaves its partial tile in its shared memory (the stages,
+// by then free), and CTA r adds up the rows r * rows / S .. of all of them in the
+// order of their k, so a result does not depend on which CTA was first.
+namespace split {
 constexpr int BN = 128;
 constexpr int THREADS = 192;
-constexpr int STAGES = 4;
+constexpr int STAGES = 3;
+constexpr int MAX_SPLIT = 8;
 constexpr int A_BYTES = BM * BKB, B_BYTES = BN * BKB;
+constexpr uint32_t TCOLS = 256;  // of each CTA's tensor memory
+constexpr uint32_t SF_COL0 = BN;
 
 template <int FMT>
 struct Tile {
   static constexpr int SF_BYTES = Kb<FMT>::CHUNKS * SF;  // of A or W, one k-block
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 2 * SF_BYTES;
-  static constexpr int NUM_BARS = 2 * STAGES + 4 + 1;
+  static constexpr int NUM_BARS = 2 * STAGES + 1;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + NUM_BARS * 8 + 16;
-  static constexpr uint32_t SF_COL0 = 2 * BN;
   static constexpr uint32_t SF_COLS = 8 * Kb<FMT>::CHUNKS;  // per stage: A, then W
 };
-static_assert(Tile<kFp4Nv>::SF_COL0 + STAGES * Tile<kFp4Nv>::SF_COLS <= TMEM_COLS, "TMEM budget");
+static_assert(SF_COL0 + STAGES * Tile<kFp4Nv>::SF_COLS <= TCOLS, "TMEM budget");
 static_assert(Tile<kFp4Nv>::STAGE_BYTES % 1024 == 0 && Tile<kFp4Mx>::STAGE_BYTES % 1024 == 0,
               "stages start on swizzle atoms");
+static_assert(2 * (Tile<kFp4Nv>::SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
+static_assert(BM * BN * 4 <= STAGES * Tile<kFp4Mx>::STAGE_BYTES, "a partial tile fits the stages");
+
+// A row's 32 values to global memory.
+template <int FMT, int EPI>
+H3_DEV void store32(const Fp4GemmParams &p, const Fp4Tensor &to, const float (&v)[32], int row,
+                    int col) {
+  const size_t at = static_cast<size_t>(row) * p.n + col;
+  if constexpr (EPI == kEpiGatedResidual) {
+    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) o[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  } else if constexpr (EPI == kEpiGeluFp4) {
+    store_fp4<FMT>(p, to, v, row, col);
+  } else {
+    store_bf16_row<32>(static_cast<uint16_t *>(p.out) + at, v);
+  }
+}
 
 template <int FMT, int EPI>
-__global__ void __launch_bounds__(THREADS, 1)
-    gemm_fp4(const __grid_constant__ CUtensorMap tma_a, const __grid_constant__ CUtensorMap tma_b,
-             const Fp4GemmParams p) {
+__global__ void __launch_bounds__(THREADS, 2)
+    gemm_fp4_split(const __grid_constant__ CUtensorMap tma_a,
+                   const __grid_constant__ CUtensorMap tma_b, const Fp4GemmParams p, int splits,
+                   int a_rows) {
   using T = Tile<FMT>;
   constexpr bool NV = FMT == kFp4Nv;
   extern __shared__ uint8_t smem_raw[];
@@ -183,201 +201,235 @@ __global__ void __launch_bounds__(THREADS, 1)
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + STAGES * T::STAGE_BYTES);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + T::NUM_BARS);
+  __shared__ int entry_status;
 
-  __shared__ int aborted;
-  if (grid_aborted(p.status, &aborted)) return;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(smem);
   const uint32_t bar0 = smem_u32(bars);
   auto FULL = [&](int s) { return bar0 + 8u * s; };
   auto EMPTY = [&](int s) { return bar0 + 8u * (STAGES + s); };
-  auto TFULL = [&](int a) { return bar0 + 8u * (2 * STAGES + a); };
-  auto TEMPTY = [&](int a) { return bar0 + 8u * (2 * STAGES + 2 + a); };
-  const uint32_t DRAIN = bar0 + 8u * (2 * STAGES + 4);
+  const uint32_t TFULL = bar0 + 8u * (2 * STAGES);
 
   if (threadIdx.x == 0) {
+    entry_status = *reinterpret_cast<const volatile int *>(p.status);
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(FULL(s), 1);
       mbar_init(EMPTY(s), 1);
     }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(TFULL(a), 1);
-      mbar_init(TEMPTY(a), 128);
-    }
-    mbar_init(DRAIN, 1);
+    mbar_init(TFULL, 1);
     fence_mbar_init();
     tma_prefetch_desc(&tma_a);
     tma_prefetch_desc(&tma_b);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+    tmem_alloc(smem_u32(tmem_slot), TCOLS);
     tmem_relinquish();
   }
+  __syncwarp();
   tc_fence_before();
-  __syncthreads();
+  if (splits > 1)
+    cluster_sync();
+  else
+    __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  // whether to run at all is decided for the cluster as a whole, by its first CTA
+  const bool skip =
+      (splits > 1 ? static_cast<int>(ld_shared_cluster_u32(map_to_cta(smem_u32(&entry_status), 0)))
+                  : entry_status) != 0;
 
-  const int num_tiles = p.tiles_m * p.tiles_n;
+  const int part = splits > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tile = blockIdx.x / splits;
+  int tm, tn;
+  tile_coords(tile, p.tiles_m, p.tiles_n, tm, tn);
   const int kblocks = (p.k + BK - 1) / BK;
+  const int kb0 = static_cast<int>(static_cast<long long>(kblocks) * part / splits);
+  const int kb1 = static_cast<int>(static_cast<long long>(kblocks) * (part + 1) / splits);
 
-  if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      long long issued = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-        int tm, tn;
-        tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait(EMPTY(stage), phase ^ 1, p.status)) {
-            ok = false;
-            break;
-          }
-          const int c0 = kb * Kb<FMT>::CHUNKS;
-          const uint32_t sf_bytes = min(Kb<FMT>::CHUNKS, p.chunks - c0) * SF;
-          // a box counts whole, also where it reads past the matrix
-          mbar_arrive_expect_tx(FULL(stage), A_BYTES + B_BYTES + 2 * sf_bytes);
-          const uint32_t sa = sbase + stage * T::STAGE_BYTES;
-          tma_load_2d(sa, &tma_a, kb * BKB, tm * BM, FULL(stage));
-          tma_load_2d(sa + A_BYTES, &tma_b, kb * BKB, tn * BN, FULL(stage));
-          bulk_load(sa + A_BYTES + B_BYTES,
-                    p.a_sf + (static_cast<size_t>(tm) * p.chunks + c0) * SF, sf_bytes, FULL(stage));
-          bulk_load(sa + A_BYTES + B_BYTES + T::SF_BYTES,
-                    p.b_sf + (static_cast<size_t>(tn) * p.chunks + c0) * SF, sf_bytes, FULL(stage));
-          ++issued;
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
+  if (!skip && warp == 0) {
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait_warp(EMPTY(stage), phase ^ 1, p.status)) break;
+      ++issued;
+      if (elect_one()) {
+        const int c0 = kb * Kb<FMT>::CHUNKS;
+        const uint32_t sf_bytes = min(Kb<FMT>::CHUNKS, p.chunks - c0) * SF;
+        // a box counts whole, also where it reads past the matrix
+        mbar_arrive_expect_tx(FULL(stage), a_rows * BKB + B_BYTES + 2 * sf_bytes);
+        const uint32_t sa = sbase + stage * T::STAGE_BYTES;
+        tma_load_2d(sa + A_BYTES, &tma_b, kb * BKB, tn * BN, FULL(stage));
+        bulk_load(sa + A_BYTES + B_BYTES + T::SF_BYTES,
+                  p.b_sf + (static_cast<size_t>(tn) * p.chunks + c0) * SF, sf_bytes, FULL(stage));
+        tma_load_2d(sa, &tma_a, kb * BKB, tm * BM, FULL(stage));
+        bulk_load(sa + A_BYTES + B_BYTES,
+                  p.a_sf + (static_cast<size_t>(tm) * p.chunks + c0) * SF, sf_bytes, FULL(stage));
       }
-      for (int i = 0; i < STAGES && i < issued; ++i) {
-        if (--stage < 0) {
-          stage = STAGES - 1;
-          phase ^= 1;
-        }
-        mbar_wait(FULL(stage), phase, p.status, false);
+      __syncwarp();
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int acc = 0;
-      uint32_t acc_phase = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-        if (!mbar_wait(TEMPTY(acc), acc_phase ^ 1, p.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait(FULL(stage), phase, p.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t sa = sbase + stage * T::STAGE_BYTES;
-          const uint32_t sb = sa + A_BYTES;
-          const uint32_t sfa = tmem + T::SF_COL0 + T::SF_COLS * stage;
-          const uint32_t sfb = sfa + 4 * Kb<FMT>::CHUNKS;
-          const int groups = min(4, (p.k - kb * BK) / 64);
-#pragma unroll
-          for (int c = 0; c < Kb<FMT>::CHUNKS; ++c) {
-            if (c * Kb<FMT>::PER_CHUNK >= groups) break;
-            tmem_cp_sf(sfa + 4 * c, desc_sf_copy(sb + B_BYTES + c * SF));
-            tmem_cp_sf(sfb + 4 * c, desc_sf_copy(sb + B_BYTES + T::SF_BYTES + c * SF));
-          }
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            if (g >= groups) break;
-            const int c = g / Kb<FMT>::PER_CHUNK, id = 2 * (g % Kb<FMT>::PER_CHUNK);
-            umma_fp4<NV>(d, desc_sw128(sa + g * 32, 16, 1024), desc_sw128(sb + g * 32, 16, 1024),
-                         idesc_fp4(BM, BN, NV, id), sfa + 4 * c, sfb + 4 * c,
-                         (kb | g) != 0 ? 1u : 0u);
-          }
-          umma_commit(EMPTY(stage));
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
-        if (!ok) break;
-        umma_commit(TFULL(acc));
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1;
-      }
-      umma_commit(DRAIN);
-      mbar_wait(DRAIN, 0, p.status, false);
-    }
-  } else {
-    const int sub = warp & 3;
-    const Alpha al = tensor_alpha(p.a_scale, p.b_scale);
-    Fp4Tensor to{};
-    if constexpr (EPI == kEpiGeluFp4) to = fp4_tensor(FMT == kFp4Nv ? p.out_scale : nullptr);
-    int acc = 0;
-    uint32_t acc_phase = 0;
-    for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
-      int tm, tn;
-      tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
-      const bool ok = mbar_wait(TFULL(acc), acc_phase, p.status);
-      if (!__all_sync(0xffffffffu, ok)) break;
+    // every load has landed before the CTA may leave (the MMA warp may have given up)
+    for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i)
+      mbar_wait(FULL(i % STAGES), (i / STAGES) & 1, p.status, false);
+  } else if (!skip && warp == 1) {
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!mbar_wait_warp(FULL(stage), phase, p.status)) break;
       tc_fence_after();
-      const uint32_t tbase =
-          tmem + (static_cast<uint32_t>(sub * 32) << 16) + static_cast<uint32_t>(acc * BN);
-      const int row = tm * BM + sub * 32 + lane;
+      const uint32_t sa = sbase + stage * T::STAGE_BYTES;
+      const uint64_t da = desc_sw128(sa, 16, 1024), db = desc_sw128(sa + A_BYTES, 16, 1024);
+      const uint64_t dsf = desc_sf_copy(sa + A_BYTES + B_BYTES);
+      const uint32_t sfa = tmem + SF_COL0 + T::SF_COLS * stage;
+      const uint32_t sfb = sfa + 4 * Kb<FMT>::CHUNKS;
+      const int groups = min(4, (p.k - kb * BK) / 64);
+      if (elect_one()) {
+#pragma unroll
+        for (int c = 0; c < Kb<FMT>::CHUNKS; ++c) {
+          if (c * Kb<FMT>::PER_CHUNK >= groups) break;
+          tmem_cp_sf(sfa + 4 * c, dsf + c * SF / 16);
+          tmem_cp_sf(sfb + 4 * c, dsf + (T::SF_BYTES + c * SF) / 16);
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (g >= groups) break;
+          const int c = g / Kb<FMT>::PER_CHUNK, id = 2 * (g % Kb<FMT>::PER_CHUNK);
+          umma_fp4<NV>(tmem, da + 2 * g, db + 2 * g, idesc_fp4(BM, BN, NV, id), sfa + 4 * c,
+                       sfb + 4 * c, (kb != kb0 || g != 0) ? 1u : 0u);
+        }
+        umma_commit(EMPTY(stage));
+      }
+      __syncwarp();
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (elect_one()) umma_commit(TFULL);
+    __syncwarp();
+    mbar_wait(TFULL, 0, p.status, false);  // no MMA is left when tensor memory is released
+  } else if (!skip) {
+    const int sub = warp & 3;
+    const int in_tile = sub * 32 + lane;
+    const int rows = min(BM, p.m - tm * BM);
+    const bool ok = mbar_wait(TFULL, 0, p.status, false);
+    tc_fence_after();
+    if (__all_sync(0xffffffffu, ok) && sub * 32 < rows) {
+      const uint32_t tbase = tmem + (static_cast<uint32_t>(sub * 32) << 16);
+      if (splits == 1) {
+        const Alpha al = tensor_alpha(p.a_scale, p.b_scale);
+        Fp4Tensor to{};
+        if constexpr (EPI == kEpiGeluFp4) to = fp4_tensor(FMT == kFp4Nv ? p.out_scale : nullptr);
+        const int row = tm * BM + in_tile;
 #pragma unroll 1
-      for (int c = 0; c < BN && tn * BN + c < p.n; c += 32) {
-        const int col = tn * BN + c;
-        Resid32 x{};
-        if (EPI == kEpiGatedResidual && row < p.m) x = load_resid(p, row, col);
-        uint32_t r[32];
-        tmem_ld32(tbase + c, r);
-        float v[32];
-        values32<EPI>(p, al, r, col, x, v);
-        if (row >= p.m) continue;
-        const size_t at = static_cast<size_t>(row) * p.n + col;
-        if constexpr (EPI == kEpiGatedResidual) {
-          float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
+        for (int c = 0; c < BN && tn * BN + c < p.n; c += 32) {
+          const int col = tn * BN + c;
+          float4 x[8] = {};  // loaded before the first store: out may be resid
+          if (EPI == kEpiGatedResidual && in_tile < rows) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              x[q] = reinterpret_cast<const float4 *>(p.resid + static_cast<size_t>(row) * p.n + col)[q];
+          }
+          uint32_t r[32];
+          tmem_ld32(tbase + c, r);
+          float v[32];
+          values32<EPI>(p, al, r, col, [&](int q) { return x[q]; }, v);
+          if (in_tile < rows) store32<FMT, EPI>(p, to, v, row, col);
+        }
+      } else {
+        // 16-byte unit q of a row at q ^ (row % 8)
+        const uint32_t o = sbase + in_tile * BN * 4;
+#pragma unroll 1
+        for (int c = 0; c < BN; c += 32) {
+          uint32_t r[32];
+          tmem_ld32(tbase + c, r);
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            o[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        } else if constexpr (EPI == kEpiGeluFp4) {
-          store_fp4<FMT>(p, to, v, row, col);
-        } else {
-          store_bf16_row<32>(static_cast<uint16_t *>(p.out) + at, v);
+            st_shared_v4(o + 16 * ((c / 4 + q) ^ (in_tile & 7)), r[4 * q], r[4 * q + 1],
+                         r[4 * q + 2], r[4 * q + 3]);
         }
       }
-      tc_fence_before();
-      mbar_arrive(TEMPTY(acc));
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1;
     }
   }
-
-  tc_fence_before();
-  __syncthreads();
+  if (splits > 1) {
+    __syncwarp();
+    cluster_sync();  // every partial tile is in its shared memory
+    if (!skip && warp >= 2) {
+      const Alpha al = tensor_alpha(p.a_scale, p.b_scale);
+      Fp4Tensor to{};
+      if constexpr (EPI == kEpiGeluFp4) to = fp4_tensor(FMT == kFp4Nv ? p.out_scale : nullptr);
+      const int rows = min(BM, p.m - tm * BM);
+      const int r0 = rows * part / splits, r1 = rows * (part + 1) / splits;
+      const int cols = min(BN, p.n - tn * BN) / 32;
+      for (int it = threadIdx.x - 64; it < (r1 - r0) * cols; it += 128) {
+        const int in_tile = r0 + it / cols, c = it % cols * 32;
+        const int row = tm * BM + in_tile, col = tn * BN + c;
+        float4 x[8] = {};
+        if (EPI == kEpiGatedResidual) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            x[q] = reinterpret_cast<const float4 *>(p.resid + static_cast<size_t>(row) * p.n + col)[q];
+        }
+        float sum[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) sum[i] = 0.f;
+        for (int s = 0; s < splits; ++s) {
+          const uint32_t o = map_to_cta(sbase, s) + in_tile * BN * 4;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 v = ld_shared_cluster_v4(o + 16 * ((c / 4 + q) ^ (in_tile & 7)));
+            sum[4 * q + 0] += v.x;
+            sum[4 * q + 1] += v.y;
+            sum[4 * q + 2] += v.z;
+            sum[4 * q + 3] += v.w;
+          }
+        }
+        uint32_t r[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(sum[i]);
+        float v[32];
+        values32<EPI>(p, al, r, col, [&](int q) { return x[q]; }, v);
+        store32<FMT, EPI>(p, to, v, row, col);
+      }
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();  // no CTA leaves while another reads its shared memory
+  } else {
+    tc_fence_before();
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, TMEM_COLS);
+    tmem_dealloc(tmem, TCOLS);
   }
 }
 
 template <int FMT, int EPI>
-cudaError_t launch(const CUtensorMap &a, const CUtensorMap &b, const Fp4GemmParams &p, int grid,
+cudaError_t launch(const Fp4GemmMaps &t, const Fp4GemmParams &p, const Fp4GemmPlan &plan,
                    cudaStream_t s) {
   static PerDevice smem_attr;
-  cudaError_t e = set_smem_once(smem_attr, gemm_fp4<FMT, EPI>, Tile<FMT>::SMEM_BYTES);
+  cudaError_t e = set_smem_once(smem_attr, gemm_fp4_split<FMT, EPI>, Tile<FMT>::SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  gemm_fp4<FMT, EPI><<<grid, THREADS, Tile<FMT>::SMEM_BYTES, s>>>(a, b, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(plan.grid, 1, 1);
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = Tile<FMT>::SMEM_BYTES;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = plan.splits;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, gemm_fp4_split<FMT, EPI>, t.a, t.b, p, plan.splits, plan.box_a);
 }
-}  // namespace one
+}  // namespace split
 
 // ------------------------------------------------------- a pair of CTAs per tile
 // Output tiles of 256 x 256 on clusters of two CTAs (M256 N256 K64): each CTA
@@ -614,16 +666,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       auto finish = [&](int j, const uint32_t (&r)[32]) {
         const int col = col0 + 32 * j;
         if (col >= p.n || row0 >= p.m) return;  // the same for the whole warp
-        Resid32 x{};
         const uint32_t o = out0 + lane * 128;  // 128-byte swizzle: 16-byte unit q at q ^ (row % 8)
         if constexpr (EPI == kEpiGatedResidual) {
           cp_async_wait_all();
           __syncwarp();
-#pragma unroll
-          for (int q = 0; q < 8; ++q) x.x[q] = ld_shared_v4(o + 16 * (q ^ (lane & 7)));
         }
         float v[32];
-        values32<EPI>(p, al, r, col, x, v);
+        values32<EPI>(p, al, r, col, [&](int q) { return ld_shared_v4(o + 16 * (q ^ (lane & 7))); }, v);
         if constexpr (EPI == kEpiGeluFp4) {
           if (row < p.m) store_fp4<FMT>(p, to, v, row, col);
         } else if constexpr (EPI == kEpiGatedResidual) {
@@ -736,7 +785,7 @@ template <int FMT, int EPI>
 cudaError_t launch_epi(const Fp4GemmMaps &t, const Fp4GemmParams &p, const Fp4GemmPlan &plan,
                        cudaStream_t s) {
   return plan.pair ? pair::launch<FMT, EPI>(t, p, plan.grid, s)
-                   : one::launch<FMT, EPI>(t.a, t.b, p, plan.grid, s);
+                   : split::launch<FMT, EPI>(t, p, plan, s);
 }
 
 template <int FMT>
@@ -761,16 +810,25 @@ cudaError_t launch_fmt(int epi, const Fp4GemmMaps &t, const Fp4GemmParams &p,
 Fp4GemmPlan fp4_gemm_plan(int fmt, Fp4GemmParams *p, int num_sms) {
   Fp4GemmPlan plan{};
   p->chunks = fp4_chunks(fmt, p->k);
-  // more than one block of 128 rows: pairs, which halve W's traffic per SM
+  const int kblocks = (p->k + BK - 1) / BK;
+  plan.splits = 1;
   plan.pair = p->m > BM;
-  plan.box_a = BM;
-  plan.box_b = plan.pair ? pair::BN / 2 : one::BN;
-  const int bm = plan.pair ? 2 * BM : BM, bn = plan.pair ? pair::BN : one::BN;
+  const int bm = plan.pair ? 2 * BM : BM, bn = plan.pair ? pair::BN : split::BN;
   p->tiles_m = (p->m + bm - 1) / bm;
   p->tiles_n = (p->n + bn - 1) / bn;
   const long long tiles = static_cast<long long>(p->tiles_m) * p->tiles_n;
-  const int most = plan.pair ? num_sms / 2 : num_sms;
-  plan.grid = static_cast<int>(tiles < most ? tiles : most) * (plan.pair ? 2 : 1);
+  plan.box_b = split::BN;
+  static_assert(split::BN == pair::BN / 2, "one box of W for both");
+  if (plan.pair) {
+    plan.box_a = BM;
+    plan.grid = 2 * static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
+  } else {
+    plan.box_a = p->m < BM ? (p->m + 7) / 8 * 8 : BM;  // no rows that are not there
+    while (plan.splits < split::MAX_SPLIT && tiles * (plan.splits + 1) <= 2 * num_sms &&
+           kblocks / (plan.splits + 1) >= 2)
+      ++plan.splits;
+    plan.grid = static_cast<int>(tiles * plan.splits);
+  }
   return plan;
 }
 

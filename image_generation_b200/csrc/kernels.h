@@ -240,9 +240,10 @@ struct Fp4GemmParams {
   int gelu_tanh;
   int *status;
 };
-// Rows of the A and W boxes and how many CTAs the launch takes.
+// Rows of the A and W boxes, CTAs of the launch, and which kernel: pairs of CTAs
+// on 256 x 256 tiles, or clusters of `splits` CTAs that share a 128 x 128 tile's k.
 struct Fp4GemmPlan {
-  int box_a, box_b, grid;
+  int box_a, box_b, grid, splits;
   bool pair;
 };
 Fp4GemmPlan fp4_gemm_plan(int fmt, Fp4GemmParams *p, int num_sms);

@@ -166,7 +166,9 @@ def operand(fmt, rows, k, seed, exact, g=None):
 
 
 SHAPES = [(1, 32, 64), (1, 64, 128), (3, 96, 192), (128, 128, 256), (129, 160, 320), (200, 768, 832),
-          (127, 2304, 768), (288, 2304, 768), (257, 416, 5376), (640, 1056, 448)]
+          (127, 2304, 768), (288, 2304, 768), (257, 416, 5376), (640, 1056, 448),
+          # k shared by clusters of 2 to 8 CTAs: even and uneven shares, rows fewer and more than CTAs
+          (1, 96, 5376), (3, 256, 1088), (100, 160, 7104), (17, 416, 2112), (128, 64, 4160), (7, 32, 3904)]
 
 
 @FMTS
