@@ -305,16 +305,19 @@ def _bad(msg: str) -> "H3DitError":
 
 def _arg(dev, t, what: str, dtypes, shape=None, dense: bool = True) -> int | None:
     """Device address of an argument of the FP4, norm and rotary calls: on the
-    context's device, of one of `dtypes`, of `shape` (None in it: any), and
-    contiguous (dense) or with contiguous rows."""
+    context's device, of one of `dtypes`, of `shape`, and contiguous (dense) or
+    with contiguous rows that do not overlap."""
     if t is None:
         return None
+    # the usual case in as few calls as can be: small launches wait for this
+    if (t.dtype in dtypes and t.get_device() == dev.index and (shape is None or t.shape == shape)
+            and t.is_contiguous()):
+        return t.data_ptr()
     if t.device != dev:
         raise _bad(f"{what} is on {t.device}, the context on {dev}")
     if t.dtype not in dtypes:
         raise _bad(f"{what} has dtype {t.dtype}")
-    if shape is not None and (t.dim() != len(shape) or any(
-            w is not None and w != s for w, s in zip(shape, t.shape))):
+    if shape is not None and t.shape != shape:
         raise _bad(f"{what} has shape {tuple(t.shape)}, not {shape}")
     if dense:
         if not t.is_contiguous():
@@ -323,6 +326,14 @@ def _arg(dev, t, what: str, dtypes, shape=None, dense: bool = True) -> int | Non
             t.shape[0] > 1 and t.stride(0) < t.shape[1]):
         raise _bad(f"{what} needs rows of consecutive elements that do not overlap")
     return t.data_ptr()
+
+
+def _matrix(t, what: str) -> Tuple[int, int]:
+    if t is None:
+        raise _bad(f"{what} is needed")
+    if t.dim() != 2:
+        raise _bad(f"{what} has shape {tuple(t.shape)}, not [rows, columns]")
+    return t.shape
 
 
 def _ld(t, width: int) -> int:
@@ -576,16 +587,20 @@ class Context:
         """The stream of a call on the context's device, which has to be current."""
         import torch
 
-        dev = self.workspace.device
-        if torch.cuda.current_device() != dev.index:
-            raise _bad(f"the context lives on {dev}, the current device is "
+        index = self.workspace.device.index
+        if torch.cuda.current_device() != index:
+            raise _bad(f"the context lives on cuda:{index}, the current device is "
                        f"cuda:{torch.cuda.current_device()}")
-        return _stream(stream)
+        if stream is not None:
+            return stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(index)  # current_stream() without its object
 
     def _scalar(self, t, what: str) -> int | None:
+        if t is None:
+            return None
         import torch
 
-        if t is not None and t.numel() != 1:
+        if t.numel() != 1:
             raise _bad(f"{what} is not one number")
         return _arg(self.workspace.device, t, what, (torch.float32,))
 
@@ -599,23 +614,23 @@ class Context:
         if q is None or sf is None:
             raise _bad(f"{what}: codes and scales are both needed")
         ptrs = _arg(dev, q, what, u8, (rows, k // 2)), _arg(dev, sf, what + " scales", u8)
-        if sf.numel() < fp4_scale_bytes(fmt, rows, k):
-            raise _bad(f"{what} scales: {sf.numel()} bytes, {fp4_scale_bytes(fmt, rows, k)} needed")
+        need = (rows + 127) // 128 * -(-k // (64 if fmt else 128)) * 512
+        if sf.numel() < need:
+            raise _bad(f"{what} scales: {sf.numel()} bytes, {need} needed")
         return ptrs
 
     def _fp4_source(self, src) -> tuple:
         import torch
 
-        ptr = _arg(self.workspace.device, src, "src", (torch.bfloat16, torch.float32), (None, None),
-                   dense=False)
-        rows, k = src.shape
+        rows, k = _matrix(src, "src")
+        ptr = _arg(self.workspace.device, src, "src", (torch.bfloat16, torch.float32), None, False)
         return ptr, int(src.dtype == torch.float32), _ld(src, k), rows, k
 
     def fp4_tensor_scale(self, src, scale_out, stream=None) -> None:
         """scale_out (one fp32) = src's largest finite magnitude over 2688 (1 if
         that is 0): what an NVFP4 matrix of src is quantized under."""
         if scale_out is None:
-            raise _bad("scale_out is None")
+            raise _bad("scale_out is needed")
         self._check(lib.h3dit_fp4_tensor_scale(self.handle, *self._fp4_source(src),
                                                self._scalar(scale_out, "scale_out"),
                                                self._here(stream)))
@@ -624,7 +639,7 @@ class Context:
         """src [rows, k] (bf16 or fp32, rows may be strided) -> codes q [rows, k/2]
         and scales sf (fp4_scale_bytes) in format H3DIT_FP4_MX or _NV."""
         source = self._fp4_source(src)
-        qp, sp = self._fp4(fmt, src.shape[0], src.shape[1], q, sf, "q")
+        qp, sp = self._fp4(fmt, source[3], source[4], q, sf, "q")
         self._check(lib.h3dit_fp4_quantize(self.handle, fmt, *source,
                                            self._scalar(tensor_scale, "tensor_scale"), qp, sp,
                                            self._here(stream)))
@@ -633,8 +648,8 @@ class Context:
         """The bf16 values [rows, k] of an FP4 matrix."""
         import torch
 
-        op = _arg(self.workspace.device, out, "out", (torch.bfloat16,), (None, None))
-        rows, k = out.shape
+        rows, k = _matrix(out, "out")
+        op = _arg(self.workspace.device, out, "out", (torch.bfloat16,))
         qp, sp = self._fp4(fmt, rows, k, q, sf, "q")
         self._check(lib.h3dit_fp4_dequantize(self.handle, fmt, qp, sp,
                                              self._scalar(tensor_scale, "tensor_scale"), rows, k,
@@ -648,11 +663,13 @@ class Context:
         import torch
 
         dev, f32 = self.workspace.device, (torch.float32,)
-        m, k = a.shape[0], 2 * a.shape[1]
-        n = w.shape[0]
+        m, k = _matrix(a, "a")
+        n, k = _matrix(w, "w")[0], 2 * k
         ap, asp = self._fp4(fmt, m, k, a, a_sf, "a")
         wp, wsp = self._fp4(fmt, n, k, w, w_sf, "w")
         osp = None
+        if out is None:
+            raise _bad("out is needed")
         if out_sf is not None:
             op, osp = self._fp4(fmt, m, n, out, out_sf, "out")
         else:
@@ -665,6 +682,29 @@ class Context:
             _arg(dev, gate, "gate", f32, (n,)), _arg(dev, resid, "resid", f32, (m, n)),
             self._here(stream)))
 
+    def _modulation(self, parts, groups: int) -> tuple:
+        """Addresses and the common row stride of gate, shift and scale."""
+        import torch
+
+        dev, f32, D = self.workspace.device, (torch.float32,), self.cfg.hidden
+        ptrs, ld = [], None
+        for name, t in parts:
+            if t is None:
+                ptrs.append(None)
+            elif t.dim() == 1:
+                if groups > 1:
+                    raise _bad(f"{name} has one row for {groups} groups")
+                ptrs.append(_arg(dev, t, name, f32, (D,)))
+            else:
+                if t.shape[0] < groups:
+                    raise _bad(f"{name} has {t.shape[0]} rows for {groups} groups")
+                ptrs.append(_arg(dev, t, name, f32, (t.shape[0], D), False))
+                if groups > 1:
+                    if ld is not None and ld != t.stride(0):
+                        raise _bad("gate, shift and scale need equal row strides")
+                    ld = t.stride(0)
+        return ptrs, ld or 0
+
     def gated_norm(self, x, x_out, out_kind: int, out, out_sf=None, out_scale=None, branch=None,
                    gate=None, shift=None, scale=None, rows_per_group: int = 0,
                    post_norm: bool = False, post_weight=None, pre_weight=None,
@@ -676,50 +716,33 @@ class Context:
         import torch
 
         dev, f32, D = self.workspace.device, (torch.float32,), self.cfg.hidden
-        if x is None or out is None:
-            raise _bad("x and out are needed")
-        xp = _arg(dev, x, "x", f32, (None, D))
-        n = x.shape[0]
-        groups = 1
+        n = _matrix(x, "x")[0]
+        if out is None:
+            raise _bad("out is needed")
         if rows_per_group < 0:
             raise _bad("rows_per_group < 0")
-        if rows_per_group > 0:
-            groups = max(1, -(-n // rows_per_group))
-        ld, mods = None, []
-        for name, t in (("gate", gate), ("shift", shift), ("scale", scale)):
-            if t is None:
-                mods.append(None)
-            elif t.dim() == 1:
-                if groups > 1:
-                    raise _bad(f"{name} has one row for {groups} groups")
-                mods.append(_arg(dev, t, name, f32, (D,)))
-            else:
-                mods.append(_arg(dev, t, name, f32, (None, D), dense=False))
-                if t.shape[0] < groups:
-                    raise _bad(f"{name} has {t.shape[0]} rows for {groups} groups")
-                if groups > 1:
-                    if ld is not None and ld != t.stride(0):
-                        raise _bad("gate, shift and scale need equal row strides")
-                    ld = t.stride(0)
-        if out_kind in (H3DIT_NORM_OUT_FP4_MX, H3DIT_NORM_OUT_FP4_NV):
-            fmt = H3DIT_FP4_MX if out_kind == H3DIT_NORM_OUT_FP4_MX else H3DIT_FP4_NV
-            op, sp = self._fp4(fmt, n, D, out, out_sf, "out")
+        rows = (n, D)
+        xp = _arg(dev, x, "x", f32, rows)
+        groups = -(-n // rows_per_group) if rows_per_group > 0 else 1
+        mods, ld = self._modulation((("gate", gate), ("shift", shift), ("scale", scale)), groups)
+        if out_kind == H3DIT_NORM_OUT_BF16:
+            op = _arg(dev, out, "out", (torch.bfloat16,), rows)
+            sp = _arg(dev, out_sf, "out_sf", (torch.uint8,))
         elif out_kind == H3DIT_NORM_OUT_MXFP8:
             op, sp = (_arg(dev, out, "out", (torch.uint8,)),
                       _arg(dev, out_sf, "out_sf", (torch.uint8,)))
             if out.numel() != n * D or out_sf is None or out_sf.numel() < mx_scale_bytes(n, D):
                 raise _bad("MXFP8 output: out or out_sf has the wrong size")
         else:
-            op = _arg(dev, out, "out", (torch.bfloat16,), (n, D))
-            sp = _arg(dev, out_sf, "out_sf", (torch.uint8,))
+            fmt = {H3DIT_NORM_OUT_FP4_MX: H3DIT_FP4_MX, H3DIT_NORM_OUT_FP4_NV: H3DIT_FP4_NV}
+            op, sp = self._fp4(fmt.get(out_kind, -1), n, D, out, out_sf, "out")
         args = h3dit_norm_args(
-            xp, _arg(dev, x_out, "x_out", f32, (n, D)),
-            _arg(dev, branch, "branch", (torch.bfloat16, torch.float32), (n, D)),
-            int(branch is not None and branch.dtype == torch.float32), int(post_norm),
+            xp, _arg(dev, x_out, "x_out", f32, rows),
+            _arg(dev, branch, "branch", (torch.bfloat16, torch.float32), rows),
+            branch is not None and branch.dtype == torch.float32, bool(post_norm),
             _arg(dev, post_weight, "post_weight", f32, (D,)),
-            _arg(dev, pre_weight, "pre_weight", f32, (D,)), mods[0], mods[1], mods[2],
-            0 if ld is None else ld, n, rows_per_group, residual_scale, out_kind, op, sp,
-            self._scalar(out_scale, "out_scale"))
+            _arg(dev, pre_weight, "pre_weight", f32, (D,)), *mods, ld, n, rows_per_group,
+            residual_scale, out_kind, op, sp, self._scalar(out_scale, "out_scale"))
         self._check(lib.h3dit_gated_norm(self.handle, C.byref(args), self._here(stream)))
 
     def rope_axes(self, spec: h3dit_rope_spec, positions, q, q_out, heads_q: int, k=None,
@@ -731,26 +754,21 @@ class Context:
         import torch
 
         dev, f32 = self.workspace.device, (torch.float32,)
-        if positions is None or positions.dim() != 2:
-            raise _bad("positions must be [n, 3]")
-        n, dh = positions.shape[0], spec.head_dim
+        n, dh = _matrix(positions, "positions")[0], spec.head_dim
         sides, dt = [], None
         for name, t, o, heads in (("q", q, q_out, heads_q), ("k", k, k_out, heads_k)):
             if heads <= 0:
-                sides.append((None, 0, None, 0, heads))
+                sides += (None, 0, None, 0, heads)
                 continue
             if t is None or o is None:
                 raise _bad(f"{name} and {name}_out are needed")
             dt = dt or t.dtype
-            types = (dt,) if dt in (torch.bfloat16, torch.float32) else ()
-            sides.append((_arg(dev, t, name, types, (n, heads * dh), dense=False),
-                          _ld(t, heads * dh),
-                          _arg(dev, o, name + "_out", types, (n, heads * dh), dense=False),
-                          _ld(o, heads * dh), heads))
+            types, shape = (dt,) if dt in (torch.bfloat16, torch.float32) else (), (n, heads * dh)
+            sides += (_arg(dev, t, name, types, shape, False), _ld(t, shape[1]),
+                      _arg(dev, o, name + "_out", types, shape, False), _ld(o, shape[1]), heads)
         self._check(lib.h3dit_rope_axes(
-            self.handle, C.byref(spec), _arg(dev, positions, "positions", f32, (None, 3)), n,
-            int(dt == torch.float32), *sides[0], *sides[1],
-            _arg(dev, q_weight, "q_weight", f32, (dh,)),
+            self.handle, C.byref(spec), _arg(dev, positions, "positions", f32, (n, 3)), n,
+            dt == torch.float32, *sides, _arg(dev, q_weight, "q_weight", f32, (dh,)),
             _arg(dev, k_weight, "k_weight", f32, (dh,)),
             H3DIT_ROPE_INVERSE if inverse else 0, self._here(stream)))
 

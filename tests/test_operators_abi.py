@@ -95,7 +95,7 @@ def test_binding_refuses_other_devices_and_shapes(host_ctx):
         (lambda: c.linear_fp4(0, 0, q, None, torch.empty(32, 64, **u8), sf, torch.empty(4, 32, **bf)), "needed"),
         (lambda: c.gated_norm(torch.empty(4, 768, **f32), None, 0, None), "needed"),
         (lambda: c.gated_norm(torch.empty(4, 770, **f32), None, 0, x), "shape"),
-        (lambda: c.rope_axes(spec, None, x, x, 1), "positions"),
+        (lambda: c.rope_axes(spec, None, x, x, 1), "positions is needed"),
         (lambda: c.rope_axes(spec, torch.empty(4, 3, **f32), x, x, 2), "shape"),
         (lambda: c.rope_axes(spec, torch.empty(4, 3, **f32), None, None, 2), "needed"),
     ]
