@@ -175,9 +175,32 @@ H3_DEV float4 ld_shared_v4(uint32_t a) {
                : "memory");
   return v;
 }
-// 16 bytes from global to shared memory, past L1, for this thread's wait.
+H3_DEV uint2 ld_shared_v2(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+// 16 bytes (past L1) or 8 from global to shared memory, for this thread's wait.
 H3_DEV void cp_async16(uint32_t dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+template <int BYTES>
+H3_DEV void cp_async(uint32_t dst, const void *src) {
+  if constexpr (BYTES == 16)
+    cp_async16(dst, src);
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
+                 : "memory");
+}
+H3_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but the newest n (1 .. 3) of this thread's groups have landed.
+H3_DEV void cp_async_wait_but(int n) {
+  if (n >= 3)
+    asm volatile("cp.async.wait_group 3;" ::: "memory");
+  else if (n == 2)
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
 }
 H3_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
