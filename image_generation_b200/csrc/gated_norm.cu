@@ -24,44 +24,61 @@ constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kRows = 4;                  // rows in shared memory per CTA, fewer where wide
 constexpr int kSmemBytes = 200 * 1024;    // of one SM, for all its CTAs
 
+// Four values as two packed pairs.
+struct Four {
+  uint64_t lo, hi;
+};
+H3_DEV Four four(float a, float b, float c, float d) { return {f2_pack(a, b), f2_pack(c, d)}; }
+H3_DEV Four four(float4 v) { return four(v.x, v.y, v.z, v.w); }
+H3_DEV float4 unpack(const Four &v) {
+  float4 r;
+  f2_unpack(v.lo, r.x, r.y);
+  f2_unpack(v.hi, r.z, r.w);
+  return r;
+}
+H3_DEV Four mul(const Four &a, const Four &b) { return {f2_mul(a.lo, b.lo), f2_mul(a.hi, b.hi)}; }
+H3_DEV Four fma(const Four &a, const Four &b, const Four &c) {
+  return {f2_fma(a.lo, b.lo, c.lo), f2_fma(a.hi, b.hi, c.hi)};
+}
+H3_DEV Four all(float v) { return four(v, v, v, v); }
+H3_DEV float sum_squares(const Four &a, const Four &b) {
+  float x, y;
+  f2_unpack(f2_fma(a.lo, a.lo, f2_fma(a.hi, a.hi, f2_fma(b.lo, b.lo, f2_mul(b.hi, b.hi)))), x, y);
+  return x + y;
+}
 // Four floats of a vector (`other` where there is none).
-H3_DEV void vec4(const float *p, int at, float other, float (&v)[4]) {
-  float4 a = make_float4(other, other, other, other);
-  if (p) a = __ldg(reinterpret_cast<const float4 *>(p + at));
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+H3_DEV Four vec4(const float *p, int at, float other) {
+  return p ? four(__ldg(reinterpret_cast<const float4 *>(p + at))) : all(other);
 }
 // Four elements in shared memory.
-H3_DEV void chunk4(uint32_t at, const float *, float (&v)[4]) {
-  const float4 a = ld_shared_v4(at);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-}
-H3_DEV void chunk4(uint32_t at, const uint16_t *, float (&v)[4]) {
+H3_DEV Four chunk4(uint32_t at, const float *) { return four(ld_shared_v4(at)); }
+H3_DEV Four chunk4(uint32_t at, const uint16_t *) {
   const uint2 a = ld_shared_v2(at);
-  v[0] = __uint_as_float(a.x << 16), v[1] = __uint_as_float(a.x & 0xffff0000u);
-  v[2] = __uint_as_float(a.y << 16), v[3] = __uint_as_float(a.y & 0xffff0000u);
+  return four(__uint_as_float(a.x << 16), __uint_as_float(a.x & 0xffff0000u),
+              __uint_as_float(a.y << 16), __uint_as_float(a.y & 0xffff0000u));
 }
 
 // Sum over the block; `red` (zero past the block's warps) is not written again
-// before another barrier has passed.
+// before another barrier has passed. Each warp adds the warps' sums up by itself.
 H3_DEV float block_sum(float v, float *red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  float t = 0.f;
-  for (int w = 0; w < static_cast<int>(blockDim.x >> 5); w += 4) {
-    const float4 q = *reinterpret_cast<const float4 *>(red + w);
-    t += (q.x + q.y) + (q.z + q.w);
-  }
-  return t;
+  v = red[threadIdx.x & 31];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
 }
 
 // Chunk `c` of a row in the output's type. Every lane of the warp calls it; `on`
 // is the same for the lanes that share a scale block.
 template <int OUT>
 H3_DEV void store_chunk(const GatedNormParams &p, const Fp4Tensor &t, int row, int c, bool on,
-                        const float (&v)[4]) {
+                        const Four &value) {
   const size_t at = static_cast<size_t>(row) * p.d + 4 * c;
+  const float4 f = unpack(value);
+  const float v[4] = {f.x, f.y, f.z, f.w};
   if constexpr (OUT == kNormBf16) {
     if (on)
       *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
@@ -136,26 +153,23 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   for (int i = 0; i < depth - 1; ++i)
     fetch(blockIdx.x + static_cast<long long>(i) * gridDim.x, i);
 
-  float gw[2][4], mul[2][4], add[2][4];  // gate post_weight, pre_weight (1 + scale), shift
-#pragma unroll
-  for (int i = 0; i < 8; ++i) gw[i / 4][i % 4] = mul[i / 4][i % 4] = add[i / 4][i % 4] = 0.f;
-  int group = -1, slot = 0;
+  // gate post_weight, pre_weight (1 + scale), shift of the columns of this thread
+  Four gw[2] = {all(0.f), all(0.f)}, up[2] = {all(0.f), all(0.f)}, add[2] = {all(0.f), all(0.f)};
+  const Four rs = all(p.residual_scale);
+  long long group_end = 0;  // first row past the modulation in hand
+  int slot = 0;
   for (int row = blockIdx.x; row < p.n; row += gridDim.x) {
-    const int g = row / p.rows_per_group;
-    if (g != group) {
-      group = g;
+    if (row >= group_end) {
+      const int g = row / p.rows_per_group;
+      group_end = (g + 1LL) * p.rows_per_group;
       const size_t mod = static_cast<size_t>(g) * p.ld_mod;
       auto load = [&](int j, int c) {
-        float w[4];
-        vec4(p.gate ? p.gate + mod : nullptr, 4 * c, 1.f, gw[j]);
-        vec4(p.post_weight, 4 * c, 1.f, w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) gw[j][i] *= w[i];
-        vec4(p.scale ? p.scale + mod : nullptr, 4 * c, 0.f, mul[j]);
-        vec4(p.pre_weight, 4 * c, 1.f, w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mul[j][i] = w[i] * (1.f + mul[j][i]);
-        vec4(p.shift ? p.shift + mod : nullptr, 4 * c, 0.f, add[j]);
+        gw[j] = mul(vec4(p.gate ? p.gate + mod : nullptr, 4 * c, 1.f), vec4(p.post_weight, 4 * c, 1.f));
+        const Four w = vec4(p.pre_weight, 4 * c, 1.f);
+        const Four one = all(1.f);
+        const Four sc = vec4(p.scale ? p.scale + mod : nullptr, 4 * c, 0.f);
+        up[j] = mul(w, fma(sc, one, one));
+        add[j] = vec4(p.shift ? p.shift + mod : nullptr, 4 * c, 0.f);
       };
       if (on0) load(0, c0);
       if (on1) load(1, c1);
@@ -163,47 +177,31 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     // the slot that the row before this one left
     fetch(row + static_cast<long long>(depth - 1) * gridDim.x, slot == 0 ? depth - 1 : slot - 1);
     cp_async_wait_but(depth - 1);
-    float x[2][4], y[2][4];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i / 4][i % 4] = y[i / 4][i % 4] = 0.f;
+    Four x[2] = {all(0.f), all(0.f)}, y[2] = {all(0.f), all(0.f)};
     {
       const uint32_t at = rows0 + slot * row_bytes, by = at + 4 * p.d;
-      if (on0) chunk4(at + 16 * c0, p.x, x[0]);
-      if (on1) chunk4(at + 16 * c1, p.x, x[1]);
-      if (branch && on0) chunk4(by + 4 * sizeof(TB) * c0, branch, y[0]);
-      if (branch && on1) chunk4(by + 4 * sizeof(TB) * c1, branch, y[1]);
+      if (on0) x[0] = chunk4(at + 16 * c0, p.x);
+      if (on1) x[1] = chunk4(at + 16 * c1, p.x);
+      if (branch && on0) y[0] = chunk4(by + 4 * sizeof(TB) * c0, branch);
+      if (branch && on1) y[1] = chunk4(by + 4 * sizeof(TB) * c1, branch);
     }
     if (++slot == depth) slot = 0;
     if (post) {
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) ss = fmaf(y[i / 4][i % 4], y[i / 4][i % 4], ss);
-      const float r = rsqrtf(block_sum(ss, red[0]) * inv_d + p.eps);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i / 4][i % 4] *= r;
+      const Four r = all(rsqrtf(block_sum(sum_squares(y[0], y[1]), red[0]) * inv_d + p.eps));
+      y[0] = mul(y[0], r);
+      y[1] = mul(y[1], r);
     }
-    float ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[j][i] *= p.residual_scale;
-        if (branch) x[j][i] = fmaf(gw[j][i], y[j][i], x[j][i]);
-        ss = fmaf(x[j][i], x[j][i], ss);
-      }
+    // without a branch y is 0
+    x[0] = fma(gw[0], y[0], mul(x[0], rs));
+    x[1] = fma(gw[1], y[1], mul(x[1], rs));
     if (p.x_out) {
       float4 *o = reinterpret_cast<float4 *>(p.x_out + static_cast<size_t>(row) * p.d);
-      if (on0) __stcs(o + c0, make_float4(x[0][0], x[0][1], x[0][2], x[0][3]));
-      if (on1) __stcs(o + c1, make_float4(x[1][0], x[1][1], x[1][2], x[1][3]));
+      if (on0) __stcs(o + c0, unpack(x[0]));
+      if (on1) __stcs(o + c1, unpack(x[1]));
     }
-    const float r = rsqrtf(block_sum(ss, red[1]) * inv_d + p.eps);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = fmaf(x[j][i] * r, mul[j][i], add[j][i]);
-      store_chunk<OUT>(p, t, row, j ? c1 : c0, j ? on1 : on0, v);
-    }
+    const Four r = all(rsqrtf(block_sum(sum_squares(x[0], x[1]), red[1]) * inv_d + p.eps));
+    store_chunk<OUT>(p, t, row, c0, on0, fma(mul(x[0], r), up[0], add[0]));
+    store_chunk<OUT>(p, t, row, c1, on1, fma(mul(x[1], r), up[1], add[1]));
     if (!post) __syncthreads();  // red[1] is read above; the next row writes it with no other barrier
   }
   cp_async_wait_all();
