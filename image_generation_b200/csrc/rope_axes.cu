@@ -9,11 +9,17 @@
 // is left of the head passes through. The inverse turns by -a, which is also
 // the gradient of the rotation.
 //
-// Bound by HBM: every element is read and written once. Positions are fp32, so
-// the angle is formed and reduced to a half turn in fp64 (far positions), and
-// its sine and cosine are computed once per token in shared memory for all
-// heads. A group of G lanes (a power of two >= head_dim / 16) owns one head,
-// each lane 8 pairs, so the head's sum of squares is log2(G) shuffles.
+// Bound by HBM: every element is read and written once. A warp takes a token (or
+// a share of its heads where there are few tokens): a group of G lanes (a power of
+// two >= head_dim / 16) owns one head at a time, each lane the same 8 pairs of
+// every head, so a head's sum of squares is log2(G) shuffles and the lane keeps
+// cosine and sine, times the norm's weights, in registers for all heads of the
+// token (from shared memory per head they were the bound: 181 us for 16896 tokens x
+// 112 heads x 96, now FIGURES). Positions are fp32, so the angle is formed and
+// reduced to a half turn in fp64 (far positions). A lane's next heads are on
+// their way to shared memory (cp.async, each lane its own pieces).
+#include <type_traits>
+
 #include "kernels.h"
 #include "ptx.cuh"
 
@@ -21,21 +27,48 @@ namespace h3 {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 8;  // tokens per CTA and pass
+constexpr int kPerSm = 3;  // CTAs: 80 registers a thread
 
-H3_DEV void load8(const uint16_t *p, float (&v)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4 *>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// Eight values as four packed pairs.
+struct Eight {
+  uint64_t v[4];
+};
+// Eight elements as loaded.
+template <typename T>
+struct Piece {
+  uint4 v[sizeof(T) / 2];
+};
+template <typename T>
+H3_DEV void load_piece(const T *p, Piece<T> &r) {
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+    r.v[i] = reinterpret_cast<const uint4 *>(p)[i];
+}
+H3_DEV void elements(const Piece<uint16_t> &r, float (&v)[8]) {
+  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[2 * i] = __uint_as_float(w[i] << 16);
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-H3_DEV void load8(const float *p, float (&v)[8]) {
+H3_DEV void elements(const Piece<float> &r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v[4 * i] = __uint_as_float(r.v[i].x), v[4 * i + 1] = __uint_as_float(r.v[i].y);
+    v[4 * i + 2] = __uint_as_float(r.v[i].z), v[4 * i + 3] = __uint_as_float(r.v[i].w);
+  }
+}
+H3_DEV Eight eight(const float (&v)[8]) {
+  return {f2_pack(v[0], v[1]), f2_pack(v[2], v[3]), f2_pack(v[4], v[5]), f2_pack(v[6], v[7])};
+}
+H3_DEV void floats(const Eight &e, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f2_unpack(e.v[i], v[2 * i], v[2 * i + 1]);
+}
+H3_DEV Eight shared8(const float *p) {
   const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  return {f2_pack(a.x, a.y), f2_pack(a.z, a.w), f2_pack(b.x, b.y), f2_pack(b.z, b.w)};
 }
 H3_DEV void store8(uint16_t *p, const float (&v)[8]) {
   st_global_v4(p, pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
@@ -64,46 +97,31 @@ H3_DEV Pair split_pair(const RopeAxesParams &p, int pair) {
 
 enum Order { kInterleaved, kSplit8, kSplitAny };  // kSplit8: every section a multiple of 8 pairs
 
-// The 8 pairs of one lane as (a, b).
-template <typename T, int ORDER>
-H3_DEV void load_pairs(const RopeAxesParams &p, const T *h, int u, const Pair &at, float (&a)[8],
-                       float (&b)[8]) {
+// The 8 pairs (a, b) of one lane, from two pieces of 8 elements.
+template <int ORDER>
+H3_DEV void pairs_of(const float (&x)[8], const float (&y)[8], Eight &a, Eight &b) {
   if constexpr (ORDER == kInterleaved) {
-    float x[8], y[8];
-    load8(h + 16 * u, x);
-    load8(h + 16 * u + 8, y);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = x[2 * i], b[i] = x[2 * i + 1];
-      a[4 + i] = y[2 * i], b[4 + i] = y[2 * i + 1];
-    }
-  } else if constexpr (ORDER == kSplit8) {
-    load8(h + at.lo, a);
-    load8(h + at.hi, b);
+    const float ea[8] = {x[0], x[2], x[4], x[6], y[0], y[2], y[4], y[6]};
+    const float eb[8] = {x[1], x[3], x[5], x[7], y[1], y[3], y[5], y[7]};
+    a = eight(ea), b = eight(eb);
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const Pair q = split_pair(p, 8 * u + i);
-      a[i] = load1(h + q.lo);
-      b[i] = load1(h + q.hi);
-    }
+    a = eight(x), b = eight(y);
   }
 }
 template <typename T, int ORDER>
-H3_DEV void store_pairs(const RopeAxesParams &p, T *h, int u, const Pair &at, const float (&a)[8],
-                        const float (&b)[8]) {
+H3_DEV void store_pairs(const RopeAxesParams &p, T *h, int u, int lo, int hi, const Eight &ea,
+                        const Eight &eb) {
+  float a[8], b[8];
+  floats(ea, a);
+  floats(eb, b);
   if constexpr (ORDER == kInterleaved) {
-    float x[8], y[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = a[i], x[2 * i + 1] = b[i];
-      y[2 * i] = a[4 + i], y[2 * i + 1] = b[4 + i];
-    }
-    store8(h + 16 * u, x);
-    store8(h + 16 * u + 8, y);
+    const float x[8] = {a[0], b[0], a[1], b[1], a[2], b[2], a[3], b[3]};
+    const float y[8] = {a[4], b[4], a[5], b[5], a[6], b[6], a[7], b[7]};
+    store8(h + lo, x);
+    store8(h + hi, y);
   } else if constexpr (ORDER == kSplit8) {
-    store8(h + at.lo, a);
-    store8(h + at.hi, b);
+    store8(h + lo, a);
+    store8(h + hi, b);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -114,96 +132,182 @@ H3_DEV void store_pairs(const RopeAxesParams &p, T *h, int u, const Pair &at, co
   }
 }
 
+// The 8 pairs of one lane in one head, as loaded.
 template <typename T, int ORDER>
-__global__ void __launch_bounds__(kThreads)
-    rope_axes_kernel(const __grid_constant__ RopeAxesParams p, int tokens, int g_log2) {
-  // cosines, then sines of the pairs of each token; 1 and 0 where nothing turns
-  __shared__ __align__(16) float cs[kMaxTokens][2][kRopeMaxPairs];
-  const int half = p.head_dim / 2, units = p.head_dim / 16;
+struct Pairs {
+  Piece<T> x, y;
+};
+template <typename T>
+struct Pairs<T, kSplitAny> {
+  float x[8], y[8];
+};
+template <typename T, int ORDER>
+H3_DEV void load_pairs(const RopeAxesParams &p, const T *h, int u, int lo, int hi,
+                       Pairs<T, ORDER> &r) {
+  if constexpr (ORDER == kSplitAny) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const Pair q = split_pair(p, 8 * u + i);
+      r.x[i] = load1(h + q.lo);
+      r.y[i] = load1(h + q.hi);
+    }
+  } else {
+    load_piece(h + lo, r.x);
+    load_piece(h + hi, r.y);
+  }
+}
+
+template <typename T, int ORDER, int G_LOG2>
+__global__ void __launch_bounds__(kThreads, kPerSm)
+    rope_axes_kernel(const __grid_constant__ RopeAxesParams p, int parts) {
+  __shared__ __align__(16) float cs[kThreads / 32][2][kRopeMaxPairs];  // of each warp's token
+  constexpr int GROUPS = 32 >> G_LOG2;
+  const int half = p.head_dim / 2;
   const int turning = p.sec[0] + p.sec[1] + p.sec[2];
-  const int u = threadIdx.x & ((1 << g_log2) - 1);
-  const int group = threadIdx.x >> g_log2, groups = kThreads >> g_log2;
-  const bool on = u < units;
-  Pair at{0, 0};
-  if (ORDER == kSplit8 && on) at = split_pair(p, 8 * u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int u = lane & ((1 << G_LOG2) - 1), group = lane >> G_LOG2;
+  const bool on = u < p.head_dim / 16;
+  // the lane's two pieces of 8 elements in a head
+  int lo = 16 * u, hi = 16 * u + 8;
+  if (ORDER == kSplit8 && on) {
+    const Pair at = split_pair(p, 8 * u);
+    lo = at.lo, hi = at.hi;
+  }
   const float inv_dh = 1.f / static_cast<float>(p.head_dim);
-  for (long long t0 = static_cast<long long>(blockIdx.x) * tokens; t0 < p.n;
-       t0 += static_cast<long long>(gridDim.x) * tokens) {
-    const int tn = static_cast<int>(p.n - t0 < tokens ? p.n - t0 : tokens);
-    for (int i = threadIdx.x; i < tn * half; i += kThreads) {
-      const int tok = i / half, pair = i - tok * half;
-      float c = 1.f, s = 0.f;
+  const int stride = GROUPS * p.head_dim;
+  const long long tasks = static_cast<long long>(p.n) * parts;
+  for (long long task = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp; task < tasks;
+       task += static_cast<long long>(gridDim.x) * (kThreads / 32)) {
+    const long long t = task / parts;
+    const int part = static_cast<int>(task - t * parts);
+    __syncwarp();  // cs[] of the token before has been read
+    for (int pair = lane; pair < half; pair += 32) {
+      float c = 1.f, s = 0.f;  // where nothing turns
       if (pair < turning) {
         const int axis = pair < p.sec[0] ? 0 : pair < p.sec[0] + p.sec[1] ? 1 : 2;
         // in half turns, reduced to [-1, 1] where fp32 is exact enough
-        double a = static_cast<double>(__ldg(p.pos + 3 * (t0 + tok) + axis)) * p.half_turns[pair];
+        double a = static_cast<double>(__ldg(p.pos + 3 * t + axis)) * p.half_turns[pair];
         a -= 2.0 * rint(0.5 * a);
         sincospif(static_cast<float>(a), &s, &c);
         if (p.inverse) s = -s;
       }
-      cs[tok][0][pair] = c;
-      cs[tok][1][pair] = s;
+      cs[warp][0][pair] = c;
+      cs[warp][1][pair] = s;
     }
-    __syncthreads();
+    __syncwarp();
 #pragma unroll 1
     for (int w = 0; w < 2; ++w) {
-      const int heads = p.heads[w], items = tn * heads;
-      const T *src = static_cast<const T *>(p.src[w]) + t0 * p.ld_src[w];
-      T *dst = static_cast<T *>(p.dst[w]) + t0 * p.ld_dst[w];
-      float wa[8], wb[8];
+      // this part's share of the heads, in rounds of GROUPS
+      const int heads = w ? p.heads[1] : p.heads[0];
+      const int rounds = (heads + GROUPS - 1) / GROUPS;
+      const int r0 = rounds * part / parts, r1 = rounds * (part + 1) / parts;
+      if (r0 >= r1) continue;
+      int head = r0 * GROUPS + group;  // of this lane in the round at hand
+      const T *src = w ? static_cast<const T *>(p.src[1]) + t * p.ld_src[1]
+                       : static_cast<const T *>(p.src[0]) + t * p.ld_src[0];
+      T *dst = w ? static_cast<T *>(p.dst[1]) + t * p.ld_dst[1]
+                 : static_cast<T *>(p.dst[0]) + t * p.ld_dst[0];
+      src += head * p.head_dim;
+      dst += head * p.head_dim;
+      // two rounds' loads ahead of the arithmetic
+      Pairs<T, ORDER> one{}, two{};
+      const int end = on ? min(r1 * GROUPS, heads) : 0;
+      if (head < end) load_pairs<T, ORDER>(p, src, u, lo, hi, one);
+      if (head + GROUPS < end) load_pairs<T, ORDER>(p, src + stride, u, lo, hi, two);
+      // x = a (wa c) - b (wb s), y = b (wb c) + a (wa s)
+      Eight ac = shared8(&cs[warp][0][on ? 8 * u : 0]), as = shared8(&cs[warp][1][on ? 8 * u : 0]);
+      Eight bc = ac, bs = as;
+      if (const float *weight = w ? p.weight[1] : p.weight[0]; weight && on) {
+        float wa[8], wb[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) wa[i] = wb[i] = 1.f;
-      if (p.weight[w] && on && items) load_pairs<float, ORDER>(p, p.weight[w], u, at, wa, wb);
-      // every lane takes the same number of turns: the shuffles need whole warps
-      for (int first = 0; first < items; first += groups) {
-        const int it = first + group;
-        const bool live = on && it < items;
-        const int tok = live ? it / heads : 0, head = live ? it - tok * heads : 0;
-        float a[8], b[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = b[i] = 0.f;
-        if (live)
-          load_pairs<T, ORDER>(p, src + tok * p.ld_src[w] + head * p.head_dim, u, at, a, b);
-        if (p.norm) {
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], fmaf(b[i], b[i], ss));
-          for (int o = (1 << g_log2) >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          const float r = rsqrtf(ss * inv_dh + p.eps);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) a[i] *= r * wa[i], b[i] *= r * wb[i];
+        for (int i = 0; i < 8; ++i) {
+          Pair q{16 * u + 2 * i, 16 * u + 2 * i + 1};
+          if (ORDER == kSplit8) q = {lo + i, hi + i};
+          if (ORDER == kSplitAny) q = split_pair(p, 8 * u + i);
+          wa[i] = __ldg(weight + q.lo);
+          wb[i] = __ldg(weight + q.hi);
         }
-        if (live) {
-          const float4 *c4 = reinterpret_cast<const float4 *>(&cs[tok][0][8 * u]);
-          const float4 *s4 = reinterpret_cast<const float4 *>(&cs[tok][1][8 * u]);
-          const float4 c0 = c4[0], c1 = c4[1], s0 = s4[0], s1 = s4[1];
-          const float c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-          const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+        const Eight va = eight(wa), vb = eight(wb);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float x = a[i], y = b[i];
-            a[i] = x * c[i] - y * s[i];
-            b[i] = y * c[i] + x * s[i];
-          }
-          store_pairs<T, ORDER>(p, dst + tok * p.ld_dst[w] + head * p.head_dim, u, at, a, b);
+        for (int i = 0; i < 4; ++i) {
+          ac.v[i] = f2_mul(ac.v[i], va.v[i]);
+          as.v[i] = f2_mul(as.v[i], va.v[i]);
+          bc.v[i] = f2_mul(bc.v[i], vb.v[i]);
+          bs.v[i] = f2_mul(bs.v[i], vb.v[i]);
         }
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bs.v[i] = f2_mul(bs.v[i], f2_pack(-1.f, -1.f));
+      auto turn = [&](Pairs<T, ORDER> &raw) {
+        const bool live = head < end;
+        Eight a, b;
+        if constexpr (ORDER == kSplitAny) {
+          pairs_of<ORDER>(raw.x, raw.y, a, b);
+        } else {
+          float x[8], y[8];
+          elements(raw.x, x);
+          elements(raw.y, y);
+          pairs_of<ORDER>(x, y, a, b);
+        }
+        if (head + 2 * GROUPS < end) load_pairs<T, ORDER>(p, src + 2 * stride, u, lo, hi, raw);
+        if (p.norm) {
+          uint64_t ss = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) ss = f2_fma(a.v[i], a.v[i], f2_fma(b.v[i], b.v[i], ss));
+          float s0, s1;
+          f2_unpack(ss, s0, s1);
+          s0 = live ? s0 + s1 : 0.f;
+#pragma unroll
+          for (int o = 1 << G_LOG2 >> 1; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+          s0 = rsqrtf(s0 * inv_dh + p.eps);
+          const uint64_t scale = f2_pack(s0, s0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a.v[i] = f2_mul(a.v[i], scale);
+            b.v[i] = f2_mul(b.v[i], scale);
+          }
+        }
+        if (live) {
+          Eight x, y;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x.v[i] = f2_fma(a.v[i], ac.v[i], f2_mul(b.v[i], bs.v[i]));
+            y.v[i] = f2_fma(b.v[i], bc.v[i], f2_mul(a.v[i], as.v[i]));
+          }
+          store_pairs<T, ORDER>(p, dst, u, lo, hi, x, y);
+        }
+        head += GROUPS;
+        src += stride;
+        dst += stride;
+      };
+#pragma unroll 1
+      for (int r = r0; r < r1; r += 2) {
+        turn(one);
+        if (r + 1 < r1) turn(two);
+      }
     }
-    __syncthreads();  // cs[] is rewritten for the next tokens
   }
+}
+
+template <typename T, int ORDER, int G_LOG2>
+cudaError_t launch_groups(const RopeAxesParams &p, int num_sms, cudaStream_t s) {
+  const int groups = 32 >> G_LOG2;
+  const int rounds = ((p.heads[0] > p.heads[1] ? p.heads[0] : p.heads[1]) + groups - 1) / groups;
+  // a token's heads go to several warps where there are fewer tokens than warps
+  const long long warps = static_cast<long long>(kPerSm) * num_sms * (kThreads / 32);
+  long long parts = warps / p.n;
+  parts = parts < 1 ? 1 : parts > rounds ? rounds : parts;
+  const long long want = (p.n * parts + kThreads / 32 - 1) / (kThreads / 32);
+  const int grid = static_cast<int>(want < kPerSm * num_sms ? want : kPerSm * num_sms);
+  rope_axes_kernel<T, ORDER, G_LOG2><<<grid, kThreads, 0, s>>>(p, static_cast<int>(parts));
+  return cudaGetLastError();
 }
 
 template <typename T, int ORDER>
 cudaError_t launch(const RopeAxesParams &p, int num_sms, cudaStream_t s) {
-  int g = 0;
-  while ((16 << g) < p.head_dim) ++g;
-  // several tokens per pass where there are enough of them to fill the SMs
-  int tokens = static_cast<int>(p.n / (4LL * num_sms));
-  tokens = tokens < 1 ? 1 : tokens > kMaxTokens ? kMaxTokens : tokens;
-  const long long want = (static_cast<long long>(p.n) + tokens - 1) / tokens;
-  const int grid = static_cast<int>(want < 8LL * num_sms ? want : 8LL * num_sms);
-  rope_axes_kernel<T, ORDER><<<grid, kThreads, 0, s>>>(p, tokens, g);
-  return cudaGetLastError();
+  if (p.head_dim <= 64) return launch_groups<T, ORDER, 2>(p, num_sms, s);
+  if (p.head_dim <= 128) return launch_groups<T, ORDER, 3>(p, num_sms, s);
+  return launch_groups<T, ORDER, 4>(p, num_sms, s);
 }
 
 template <typename T>
