@@ -28,36 +28,27 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPerSm = 3;  // CTAs: 80 registers a thread
+constexpr int kDepth = 4;  // rounds of heads of a warp in shared memory
 
 // Eight values as four packed pairs.
 struct Eight {
   uint64_t v[4];
 };
-// Eight elements as loaded.
-template <typename T>
-struct Piece {
-  uint4 v[sizeof(T) / 2];
-};
-template <typename T>
-H3_DEV void load_piece(const T *p, Piece<T> &r) {
-#pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
-    r.v[i] = reinterpret_cast<const uint4 *>(p)[i];
-}
-H3_DEV void elements(const Piece<uint16_t> &r, float (&v)[8]) {
-  const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
+// Eight elements in shared memory.
+H3_DEV void load8(uint32_t at, const uint16_t *, float (&v)[8]) {
+  const float4 f = ld_shared_v4(at);
+  const uint32_t w[4] = {__float_as_uint(f.x), __float_as_uint(f.y), __float_as_uint(f.z),
+                         __float_as_uint(f.w)};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[2 * i] = __uint_as_float(w[i] << 16);
     v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
 }
-H3_DEV void elements(const Piece<float> &r, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    v[4 * i] = __uint_as_float(r.v[i].x), v[4 * i + 1] = __uint_as_float(r.v[i].y);
-    v[4 * i + 2] = __uint_as_float(r.v[i].z), v[4 * i + 3] = __uint_as_float(r.v[i].w);
-  }
+H3_DEV void load8(uint32_t at, const float *, float (&v)[8]) {
+  const float4 a = ld_shared_v4(at), b = ld_shared_v4(at + 16);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 H3_DEV Eight eight(const float (&v)[8]) {
   return {f2_pack(v[0], v[1]), f2_pack(v[2], v[3]), f2_pack(v[4], v[5]), f2_pack(v[6], v[7])};
@@ -78,8 +69,8 @@ H3_DEV void store8(float *p, const float (&v)[8]) {
   reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
-H3_DEV float load1(const uint16_t *p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
-H3_DEV float load1(const float *p) { return *p; }
+H3_DEV float load1(uint32_t at, const uint16_t *) { return __uint_as_float(ld_shared_u16(at) << 16); }
+H3_DEV float load1(uint32_t at, const float *) { return __uint_as_float(ld_shared_u32(at)); }
 H3_DEV void store1(uint16_t *p, float v) { *p = static_cast<uint16_t>(pack_bf16x2(v, 0.f)); }
 H3_DEV void store1(float *p, float v) { *p = v; }
 
@@ -132,36 +123,13 @@ H3_DEV void store_pairs(const RopeAxesParams &p, T *h, int u, int lo, int hi, co
   }
 }
 
-// The 8 pairs of one lane in one head, as loaded.
-template <typename T, int ORDER>
-struct Pairs {
-  Piece<T> x, y;
-};
-template <typename T>
-struct Pairs<T, kSplitAny> {
-  float x[8], y[8];
-};
-template <typename T, int ORDER>
-H3_DEV void load_pairs(const RopeAxesParams &p, const T *h, int u, int lo, int hi,
-                       Pairs<T, ORDER> &r) {
-  if constexpr (ORDER == kSplitAny) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const Pair q = split_pair(p, 8 * u + i);
-      r.x[i] = load1(h + q.lo);
-      r.y[i] = load1(h + q.hi);
-    }
-  } else {
-    load_piece(h + lo, r.x);
-    load_piece(h + hi, r.y);
-  }
-}
-
 template <typename T, int ORDER, int G_LOG2>
 __global__ void __launch_bounds__(kThreads, kPerSm)
     rope_axes_kernel(const __grid_constant__ RopeAxesParams p, int parts) {
   __shared__ __align__(16) float cs[kThreads / 32][2][kRopeMaxPairs];  // of each warp's token
   constexpr int GROUPS = 32 >> G_LOG2;
+  constexpr uint32_t ROUND = GROUPS * (16 << G_LOG2) * sizeof(T);  // bytes of GROUPS heads, at most
+  extern __shared__ __align__(16) uint8_t ring_smem[];  // of each warp: kDepth rounds
   const int half = p.head_dim / 2;
   const int turning = p.sec[0] + p.sec[1] + p.sec[2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -175,6 +143,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   }
   const float inv_dh = 1.f / static_cast<float>(p.head_dim);
   const int stride = GROUPS * p.head_dim;
+  const uint32_t ring = smem_u32(ring_smem) + warp * kDepth * ROUND;
+  const uint32_t head_at = group * p.head_dim * sizeof(T);
+  const int round_units = stride * static_cast<int>(sizeof(T)) / 16;  // 16-byte pieces
   const long long tasks = static_cast<long long>(p.n) * parts;
   for (long long task = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp; task < tasks;
        task += static_cast<long long>(gridDim.x) * (kThreads / 32)) {
@@ -203,17 +174,30 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       const int r0 = rounds * part / parts, r1 = rounds * (part + 1) / parts;
       if (r0 >= r1) continue;
       int head = r0 * GROUPS + group;  // of this lane in the round at hand
+      const int last = min(r1 * GROUPS, heads);
+      const int end = on ? last : 0;
       const T *src = w ? static_cast<const T *>(p.src[1]) + t * p.ld_src[1]
                        : static_cast<const T *>(p.src[0]) + t * p.ld_src[0];
       T *dst = w ? static_cast<T *>(p.dst[1]) + t * p.ld_dst[1]
                  : static_cast<T *>(p.dst[0]) + t * p.ld_dst[0];
-      src += head * p.head_dim;
       dst += head * p.head_dim;
-      // two rounds' loads ahead of the arithmetic
-      Pairs<T, ORDER> one{}, two{};
-      const int end = on ? min(r1 * GROUPS, heads) : 0;
-      if (head < end) load_pairs<T, ORDER>(p, src, u, lo, hi, one);
-      if (head + GROUPS < end) load_pairs<T, ORDER>(p, src + stride, u, lo, hi, two);
+      // rounds on their way to shared memory, whole lines at a time
+      const uint8_t *from = reinterpret_cast<const uint8_t *>(src + r0 * stride) + 16 * lane;
+      int left = (last - r0 * GROUPS) * p.head_dim * static_cast<int>(sizeof(T)) / 16 - lane;
+      uint32_t to = ring;
+      auto fetch = [&] {
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(ROUND / 512); ++i)
+          if (32 * i + lane < round_units && 32 * i < left)
+            cp_async16(to + 16 * lane + 512 * i, from + 512 * i);
+        cp_async_commit();
+        from += stride * sizeof(T);
+        left -= round_units;
+        to = to == ring + (kDepth - 1) * ROUND ? ring : to + ROUND;
+      };
+      __syncwarp();  // the ring has been read
+#pragma unroll
+      for (int i = 0; i < kDepth - 1; ++i) fetch();
       // x = a (wa c) - b (wb s), y = b (wb c) + a (wa s)
       Eight ac = shared8(&cs[warp][0][on ? 8 * u : 0]), as = shared8(&cs[warp][1][on ? 8 * u : 0]);
       Eight bc = ac, bs = as;
@@ -238,25 +222,38 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) bs.v[i] = f2_mul(bs.v[i], f2_pack(-1.f, -1.f));
-      auto turn = [&](Pairs<T, ORDER> &raw) {
+      uint32_t at = ring;
+#pragma unroll 1
+      for (int r = r0; r < r1; ++r) {
+        __syncwarp();  // the round before has been read: its place is free
+        fetch();
+        cp_async_wait_but(kDepth - 1);
+        __syncwarp();  // the other lanes' copies too
         const bool live = head < end;
-        Eight a, b;
-        if constexpr (ORDER == kSplitAny) {
-          pairs_of<ORDER>(raw.x, raw.y, a, b);
-        } else {
+        Eight a{}, b{};
+        if (live) {
           float x[8], y[8];
-          elements(raw.x, x);
-          elements(raw.y, y);
+          if constexpr (ORDER == kSplitAny) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const Pair q = split_pair(p, 8 * u + i);
+              x[i] = load1(at + head_at + q.lo * sizeof(T), static_cast<const T *>(nullptr));
+              y[i] = load1(at + head_at + q.hi * sizeof(T), static_cast<const T *>(nullptr));
+            }
+          } else {
+            load8(at + head_at + lo * sizeof(T), static_cast<const T *>(nullptr), x);
+            load8(at + head_at + hi * sizeof(T), static_cast<const T *>(nullptr), y);
+          }
           pairs_of<ORDER>(x, y, a, b);
         }
-        if (head + 2 * GROUPS < end) load_pairs<T, ORDER>(p, src + 2 * stride, u, lo, hi, raw);
+        at = at == ring + (kDepth - 1) * ROUND ? ring : at + ROUND;
         if (p.norm) {
           uint64_t ss = 0;
 #pragma unroll
           for (int i = 0; i < 4; ++i) ss = f2_fma(a.v[i], a.v[i], f2_fma(b.v[i], b.v[i], ss));
           float s0, s1;
           f2_unpack(ss, s0, s1);
-          s0 = live ? s0 + s1 : 0.f;
+          s0 += s1;
 #pragma unroll
           for (int o = 1 << G_LOG2 >> 1; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
           s0 = rsqrtf(s0 * inv_dh + p.eps);
@@ -277,20 +274,20 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
           store_pairs<T, ORDER>(p, dst, u, lo, hi, x, y);
         }
         head += GROUPS;
-        src += stride;
         dst += stride;
-      };
-#pragma unroll 1
-      for (int r = r0; r < r1; r += 2) {
-        turn(one);
-        if (r + 1 < r1) turn(two);
       }
     }
   }
+  cp_async_wait_all();  // empty groups
 }
 
 template <typename T, int ORDER, int G_LOG2>
 cudaError_t launch_groups(const RopeAxesParams &p, int num_sms, cudaStream_t s) {
+  static PerDevice attr;
+  constexpr int kBytes = kDepth * (32 >> G_LOG2) * (16 << G_LOG2) * static_cast<int>(sizeof(T)) *
+                         (kThreads / 32);
+  cudaError_t e = set_smem_once(attr, rope_axes_kernel<T, ORDER, G_LOG2>, kBytes);
+  if (e != cudaSuccess) return e;
   const int groups = 32 >> G_LOG2;
   const int rounds = ((p.heads[0] > p.heads[1] ? p.heads[0] : p.heads[1]) + groups - 1) / groups;
   // a token's heads go to several warps where there are fewer tokens than warps
@@ -299,7 +296,7 @@ cudaError_t launch_groups(const RopeAxesParams &p, int num_sms, cudaStream_t s) 
   parts = parts < 1 ? 1 : parts > rounds ? rounds : parts;
   const long long want = (p.n * parts + kThreads / 32 - 1) / (kThreads / 32);
   const int grid = static_cast<int>(want < kPerSm * num_sms ? want : kPerSm * num_sms);
-  rope_axes_kernel<T, ORDER, G_LOG2><<<grid, kThreads, 0, s>>>(p, static_cast<int>(parts));
+  rope_axes_kernel<T, ORDER, G_LOG2><<<grid, kThreads, kBytes, s>>>(p, static_cast<int>(parts));
   return cudaGetLastError();
 }
 
