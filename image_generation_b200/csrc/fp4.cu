@@ -3,10 +3,13 @@
 // stands for.
 //
 // All three are bound by HBM: 2 bytes read per bf16 element and 1/2 byte plus
-// 1/32 or 1/16 written (the tensor scale only reads). One lane owns 16
-// consecutive elements, so an NVFP4 block needs no exchange between lanes and
-// an MXFP4 block one shuffle; four lanes (64 elements, what rows are a multiple
-// of) join their scale bytes into one store.
+// 1/32 or 1/16 written (the tensor scale only reads, the values are written as 2
+// bytes). One lane owns 16 consecutive elements (32 bytes of bf16 in one access),
+// so an NVFP4 block needs no exchange between lanes and an MXFP4 block one
+// shuffle; four lanes (64 elements, what rows are a multiple of) join their scale
+// bytes into one store. The quantization goes from the matrix's end to its
+// beginning: what the tensor scale's pass read last is still in L2, and what it
+// writes last is what a reader from the beginning wants first. FIGURES
 #include "fp4.cuh"
 
 namespace h3 {
@@ -14,65 +17,89 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 16 consecutive elements as fp32.
-H3_DEV void load16(const uint16_t *p, float (&v)[16]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-  const uint4 b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
-H3_DEV void load16(const float *p, float (&v)[16]) {
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p) + q);
-    v[4 * q] = a.x;
-    v[4 * q + 1] = a.y;
-    v[4 * q + 2] = a.z;
-    v[4 * q + 3] = a.w;
-  }
+// 32 bytes; `wide`: the address is a multiple of 32 (else of 16).
+H3_DEV Words8 load32(const void *p, bool wide) {
+  if (wide) return ld_global_v8(p);
+  const uint4 a = __ldg(static_cast<const uint4 *>(p));
+  const uint4 b = __ldg(static_cast<const uint4 *>(p) + 1);
+  return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
 }
 
-// Unit u (16 elements) of a [rows, k] matrix: its row and its place in it.
+// 16 consecutive elements as loaded, and as fp32.
+template <typename T>
 struct Unit {
-  long long row;
-  int at;
+  Words8 w[sizeof(T) / 2];
 };
-H3_DEV Unit unit_of(long long u, int per_row) {
-  Unit r;
-  r.row = u / per_row;
-  r.at = static_cast<int>(u - r.row * per_row);
-  return r;
+template <typename T>
+H3_DEV void load16(const T *p, bool wide, Unit<T> &u) {
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+    u.w[i] = load32(reinterpret_cast<const uint8_t *>(p) + 32 * i, wide);
 }
+H3_DEV void values16(const Unit<uint16_t> &u, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    v[2 * i] = __uint_as_float(u.w[0].v[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u.w[0].v[i] & 0xffff0000u);
+  }
+}
+H3_DEV void values16(const Unit<float> &u, float (&v)[16]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(u.w[i / 8].v[i % 8]);
+}
+bool is_wide(const void *p, long long row_bytes) {
+  return (reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(row_bytes)) % 32 == 0;
+}
+
+// Units (16 elements) of a [rows, k] matrix that one thread passes over, `step`
+// apart: the row and the place in it, kept without a division per unit.
+struct Walk {
+  long long row, dr;
+  int at, da, per_row;
+  H3_DEV Walk(long long u, long long step, int n) : per_row(n) {
+    row = u / n;
+    at = static_cast<int>(u - row * n);
+    dr = step / n;
+    da = static_cast<int>(step - dr * n);
+  }
+  H3_DEV void next() {
+    row += dr;
+    at += da;
+    if (at >= per_row) at -= per_row, ++row;
+  }
+};
 
 template <int FMT, typename T>
 __global__ void __launch_bounds__(kThreads)
-    fp4_quantize_kernel(const T *__restrict__ src, long long ld, long long units, int k,
+    fp4_quantize_kernel(const T *__restrict__ src, long long ld, bool wide, long long rows, int k,
                         const float *__restrict__ g, uint8_t *__restrict__ dst,
                         uint8_t *__restrict__ sf) {
   const Fp4Tensor t = fp4_tensor(FMT == kFp4Nv ? g : nullptr);
   const int per_row = k / 16;
   const int chunks = (k / Fp4<FMT>::BLOCK + 3) / 4;
   const long long step = static_cast<long long>(gridDim.x) * kThreads;
-  // units is a multiple of 4, so the four lanes that share a scale store stay together
-  for (long long u = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; u < units;
-       u += step) {
+  // rows count from the last one; a row is a multiple of four units, so the four
+  // lanes that share a scale store stay together
+  Walk at(static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x, step, per_row);
+  Walk ahead = at;  // the next unit is loaded before this one's arithmetic
+  Unit<T> here{};
+  if (at.row < rows) load16(src + (rows - 1 - at.row) * ld + 16 * at.at, wide, here);
+  for (; at.row < rows; at.next()) {
     const unsigned live = __activemask();
-    const Unit at = unit_of(u, per_row);
+    const long long r = rows - 1 - at.row;
     float v[16];
-    load16(src + at.row * ld + 16 * at.at, v);
+    values16(here, v);
+    ahead.next();
+    if (ahead.row < rows) load16(src + (rows - 1 - ahead.row) * ld + 16 * ahead.at, wide, here);
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) amax = amax_nan(amax, fabsf(v[i]));
     if (FMT == kFp4Mx) amax = amax_nan(amax, __shfl_xor_sync(live, amax, 1));
     float inv;
     const uint32_t sb = fp4_scale<FMT>(amax, t, &inv);
-    *reinterpret_cast<uint2 *>(dst + at.row * (k / 2) + 8 * at.at) =
+    *reinterpret_cast<uint2 *>(dst + r * (k / 2) + 8 * at.at) =
         make_uint2(fp4_pack8(v, inv), fp4_pack8(v + 8, inv));
-    const int row = static_cast<int>(at.row);
+    const int row = static_cast<int>(r);
     if (FMT == kFp4Nv) {
       uint32_t w = sb << (8 * (at.at & 3));
       w |= __shfl_xor_sync(live, w, 1);
@@ -95,31 +122,42 @@ __global__ void __launch_bounds__(kThreads)
 template <int FMT>
 __global__ void __launch_bounds__(kThreads)
     fp4_dequantize_kernel(const uint8_t *__restrict__ q, const uint8_t *__restrict__ sf,
-                          long long units, int k, const float *__restrict__ g,
-                          uint16_t *__restrict__ out) {
+                          long long rows, int k, const float *__restrict__ g,
+                          uint16_t *__restrict__ out, bool wide) {
   const float gv = g ? __ldg(g) : 1.f;
   const int per_row = k / 16;
   const int chunks = (k / Fp4<FMT>::BLOCK + 3) / 4;
   const long long step = static_cast<long long>(gridDim.x) * kThreads;
-  for (long long u = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; u < units;
-       u += step) {
-    const Unit at = unit_of(u, per_row);
-    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(q + at.row * (k / 2) + 8 * at.at));
-    const int s = FMT == kFp4Nv ? at.at : at.at >> 1;
-    const float d =
-        fp4_scale_value<FMT>(__ldg(sf + mx_sf_offset(static_cast<int>(at.row), s, chunks)), gv);
-    uint32_t o[8];
+  Walk at(static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x, step, per_row);
+  Walk ahead = at;  // the next unit is loaded before this one's arithmetic
+  uint2 w = make_uint2(0, 0);
+  uint32_t sb = 0;
+  auto load = [&](const Walk &u) {
+    w = __ldg(reinterpret_cast<const uint2 *>(q + u.row * (k / 2) + 8 * u.at));
+    sb = __ldg(sf + mx_sf_offset(static_cast<int>(u.row), FMT == kFp4Nv ? u.at : u.at >> 1, chunks));
+  };
+  if (at.row < rows) load(at);
+  for (; at.row < rows; at.next()) {
+    const uint2 codes = w;
+    const float d = fp4_scale_value<FMT>(sb, gv);
+    ahead.next();
+    if (ahead.row < rows) load(ahead);
+    Words8 o;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t b = ((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xffu;
+      const uint32_t b = ((i < 4 ? codes.x : codes.y) >> (8 * (i & 3))) & 0xffu;
       const __half2_raw h =
           __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(b), __NV_E2M1);
       const float2 f = __half22float2(__half2(h));
-      o[i] = pack_bf16x2(__fmul_rn(f.x, d), __fmul_rn(f.y, d));
+      o.v[i] = pack_bf16x2(__fmul_rn(f.x, d), __fmul_rn(f.y, d));
     }
     uint16_t *dst = out + at.row * k + 16 * at.at;
-    st_global_v4(dst, o[0], o[1], o[2], o[3]);
-    st_global_v4(dst + 8, o[4], o[5], o[6], o[7]);
+    if (wide) {
+      st_global_v8(dst, o);
+    } else {
+      st_global_v4(dst, o.v[0], o.v[1], o.v[2], o.v[3]);
+      st_global_v4(dst + 8, o.v[4], o.v[5], o.v[6], o.v[7]);
+    }
   }
 }
 
@@ -129,7 +167,7 @@ __global__ void __launch_bounds__(kThreads)
 // not depend on the order, so neither does the result.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-    fp4_tensor_scale_kernel(const T *__restrict__ src, long long ld, long long units, int k,
+    fp4_tensor_scale_kernel(const T *__restrict__ src, long long ld, bool wide, long long rows, int k,
                             float *__restrict__ part, unsigned *__restrict__ done,
                             float *__restrict__ out) {
   __shared__ float red[kThreads / 32];
@@ -137,11 +175,12 @@ __global__ void __launch_bounds__(kThreads)
   const int per_row = k / 16;
   const long long step = static_cast<long long>(gridDim.x) * kThreads;
   float m = 0.f;
-  for (long long u = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; u < units;
-       u += step) {
-    const Unit at = unit_of(u, per_row);
+  for (Walk at(static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x, step, per_row);
+       at.row < rows; at.next()) {
+    Unit<T> here;
+    load16(src + at.row * ld + 16 * at.at, wide, here);
     float v[16];
-    load16(src + at.row * ld + 16 * at.at, v);
+    values16(here, v);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float a = fabsf(v[i]);
@@ -190,8 +229,9 @@ cudaError_t launch_fp4_quantize(int fmt, const void *src, bool f32, long long ld
                                 cudaStream_t s) {
   const long long units = static_cast<long long>(rows) * (k / 16);
   const int grid = grid_for(units, num_sms);
+  const bool wide = is_wide(src, ld * (f32 ? 4 : 2));
   auto run = [&](auto kernel, auto *p) {
-    kernel<<<grid, kThreads, 0, s>>>(p, ld, units, k, g, dst, sf);
+    kernel<<<grid, kThreads, 0, s>>>(p, ld, wide, rows, k, g, dst, sf);
     return cudaGetLastError();
   };
   const float *pf = static_cast<const float *>(src);
@@ -208,10 +248,11 @@ cudaError_t launch_fp4_dequantize(int fmt, const uint8_t *q, const uint8_t *sf, 
   const long long units = static_cast<long long>(rows) * (k / 16);
   const int grid = grid_for(units, num_sms);
   uint16_t *o = static_cast<uint16_t *>(out);
+  const bool wide = is_wide(out, 2LL * k);
   if (fmt == kFp4Mx)
-    fp4_dequantize_kernel<kFp4Mx><<<grid, kThreads, 0, s>>>(q, sf, units, k, g, o);
+    fp4_dequantize_kernel<kFp4Mx><<<grid, kThreads, 0, s>>>(q, sf, rows, k, g, o, wide);
   else
-    fp4_dequantize_kernel<kFp4Nv><<<grid, kThreads, 0, s>>>(q, sf, units, k, g, o);
+    fp4_dequantize_kernel<kFp4Nv><<<grid, kThreads, 0, s>>>(q, sf, rows, k, g, o, wide);
   return cudaGetLastError();
 }
 
@@ -221,12 +262,13 @@ cudaError_t launch_fp4_tensor_scale(const void *src, bool f32, long long ld, int
   const long long units = static_cast<long long>(rows) * (k / 16);
   int grid = grid_for(units, num_sms);
   if (grid > kFp4ScaleParts) grid = kFp4ScaleParts;
+  const bool wide = is_wide(src, ld * (f32 ? 4 : 2));
   if (f32)
-    fp4_tensor_scale_kernel<<<grid, kThreads, 0, s>>>(static_cast<const float *>(src), ld, units,
+    fp4_tensor_scale_kernel<<<grid, kThreads, 0, s>>>(static_cast<const float *>(src), ld, wide, rows,
                                                       k, part, done, out);
   else
-    fp4_tensor_scale_kernel<<<grid, kThreads, 0, s>>>(static_cast<const uint16_t *>(src), ld,
-                                                      units, k, part, done, out);
+    fp4_tensor_scale_kernel<<<grid, kThreads, 0, s>>>(static_cast<const uint16_t *>(src), ld, wide,
+                                                      rows, k, part, done, out);
   return cudaGetLastError();
 }
 
