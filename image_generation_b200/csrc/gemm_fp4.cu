@@ -78,21 +78,21 @@ H3_DEV void gelu2(float &a, float &b) {
   b = fmaxf(b, 0.f) - q1;
 }
 
-// 32 accumulators of a row, as values: alpha acc + bias, then GELU, or the
+// N accumulators of a row, as values: alpha acc + bias, then GELU, or the
 // gated addition to the residual (resid(q): columns 4 q .. 4 q + 3 of it).
-template <int EPI, typename Resid>
-H3_DEV void values32(const Fp4GemmParams &p, const Alpha &al, const uint32_t (&acc)[32], int col,
-                     Resid &&resid, float (&v)[32]) {
+template <int EPI, int N, typename Resid>
+H3_DEV void values(const Fp4GemmParams &p, const Alpha &al, const uint32_t (&acc)[N], int col,
+                   Resid &&resid, float (&v)[N]) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(acc[i]) * al.a;
+  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(acc[i]) * al.a;
   if (al.b != 1.f) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] *= al.b;
+    for (int i = 0; i < N; ++i) v[i] *= al.b;
   }
   if (p.bias) {
     const float4 *b = reinterpret_cast<const float4 *>(p.bias + col);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < N / 4; ++q) {
       const float4 bb = __ldg(b + q);
       v[4 * q + 0] += bb.x;
       v[4 * q + 1] += bb.y;
@@ -103,7 +103,7 @@ H3_DEV void values32(const Fp4GemmParams &p, const Alpha &al, const uint32_t (&a
   if constexpr (EPI == kEpiGatedResidual) {
     const float4 *g = reinterpret_cast<const float4 *>(p.gate + col);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < N / 4; ++q) {
       const float4 gg = __ldg(g + q), x = resid(q);
       v[4 * q + 0] = fmaf(gg.x, v[4 * q + 0], x.x);
       v[4 * q + 1] = fmaf(gg.y, v[4 * q + 1], x.y);
@@ -111,13 +111,13 @@ H3_DEV void values32(const Fp4GemmParams &p, const Alpha &al, const uint32_t (&a
       v[4 * q + 3] = fmaf(gg.w, v[4 * q + 3], x.w);
     }
   } else if constexpr (EPI != kEpiStore) {
-    // one branch for the 32, not one each
+    // one branch for all, not one each
     if (p.gelu_tanh) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = gelu_f(v[i], 1);
+      for (int i = 0; i < N; ++i) v[i] = gelu_f(v[i], 1);
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; i += 2) gelu2(v[i], v[i + 1]);
+      for (int i = 0; i < N; i += 2) gelu2(v[i], v[i + 1]);
     }
   }
 }
@@ -141,15 +141,38 @@ H3_DEV void store_fp4(const Fp4GemmParams &p, const Fp4Tensor &t, const float (&
   }
 }
 
+// The same with 8 values in a lane: two or four neighbouring lanes (all of them
+// in `live`) share a scale block.
+template <int FMT>
+H3_DEV void store_fp4_by8(const Fp4GemmParams &p, const Fp4Tensor &t, const float (&v)[8], int row,
+                          int col, unsigned live) {
+  float am = 0.f, inv;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) am = amax_nan(am, fabsf(v[i]));
+  am = amax_nan(am, __shfl_xor_sync(live, am, 1));
+  if constexpr (FMT == kFp4Mx) am = amax_nan(am, __shfl_xor_sync(live, am, 2));
+  const uint32_t sb = fp4_scale<FMT>(am, t, &inv);
+  *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.out) +
+                                (static_cast<size_t>(row) * p.n + col) / 2) = fp4_pack8(v, inv);
+  constexpr int B = Fp4<FMT>::BLOCK;
+  if (col % B) return;
+  uint8_t *sf = p.out_sf + mx_sf_offset(row, col / B, (p.n / B + 3) / 4);
+  *sf = static_cast<uint8_t>(sb);
+  // a row that ends with two of its last four scales: the others are 0
+  if (FMT == kFp4Mx && col + B == p.n && p.n % 128 == 64) *reinterpret_cast<uint16_t *>(sf + 1) = 0;
+}
+
 // ---------------------------------------------------------- few tiles: split k
 // Output tiles of 128 x 128, one per CTA or per cluster of up to eight CTAs that
 // share its k-blocks: for few rows (where reading W bounds the call) and for
 // products with too few 256 x 256 tiles to fill the SMs. Two CTAs fit on an SM, so
 // one's epilogue runs beside the other's loads.
 //   warp 0 TMA and bulk loads, warp 1 MMAs (M128 N128 K64), warps 2..5 epilogue.
-// In a cluster each CTA leaves its partial tile in its shared memory (the stages,
-// by then free), and CTA r adds up the rows r * rows / S .. of all of them in the
-// order of their k, so a result does not depend on which CTA was first.
+// In a cluster CTA r finishes a slice of the tile's rows: the others store their
+// partial sums of those rows into its shared memory (the stages, free once every
+// CTA of the cluster has no MMA left), and it adds them up in the order of their
+// k, so a result does not depend on which CTA was first. (Reading the partial
+// tiles from the other CTAs instead waits for each load: 40 us for 128 rows.)
 namespace split {
 constexpr int BN = 128;
 constexpr int THREADS = 192;
@@ -171,7 +194,9 @@ static_assert(SF_COL0 + STAGES * Tile<kFp4Nv>::SF_COLS <= TCOLS, "TMEM budget");
 static_assert(Tile<kFp4Nv>::STAGE_BYTES % 1024 == 0 && Tile<kFp4Mx>::STAGE_BYTES % 1024 == 0,
               "stages start on swizzle atoms");
 static_assert(2 * (Tile<kFp4Nv>::SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
-static_assert(BM * BN * 4 <= STAGES * Tile<kFp4Mx>::STAGE_BYTES, "a partial tile fits the stages");
+constexpr int SLOTS_BYTES = (BM + MAX_SPLIT) * BN * 4;  // the parts of a slice of rows
+static_assert(SLOTS_BYTES + 4 * 4096 <= STAGES * Tile<kFp4Mx>::STAGE_BYTES,
+              "slots and boxes fit into the stages");
 
 // A row's 32 values to global memory.
 template <int FMT, int EPI>
@@ -337,68 +362,98 @@ __global__ void __launch_bounds__(THREADS, 2)
           uint32_t r[32];
           tmem_ld32(tbase + c, r);
           float v[32];
-          values32<EPI>(p, al, r, col, [&](int q) { return x[q]; }, v);
+          values<EPI>(p, al, r, col, [&](int q) { return x[q]; }, v);
           if (in_tile < rows) store32<FMT, EPI>(p, to, v, row, col);
-        }
-      } else {
-        // 16-byte unit q of a row at q ^ (row % 8)
-        const uint32_t o = sbase + in_tile * BN * 4;
-#pragma unroll 1
-        for (int c = 0; c < BN; c += 32) {
-          uint32_t r[32];
-          tmem_ld32(tbase + c, r);
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            st_shared_v4(o + 16 * ((c / 4 + q) ^ (in_tile & 7)), r[4 * q], r[4 * q + 1],
-                         r[4 * q + 2], r[4 * q + 3]);
         }
       }
     }
   }
   if (splits > 1) {
     __syncwarp();
-    cluster_sync();  // every partial tile is in its shared memory
+    cluster_sync();  // no MMA or load of the cluster uses the stages any more
+    const int rows = min(BM, p.m - tm * BM);
+    const int slice = (rows + splits - 1) / splits;  // rows that one CTA finishes
+    const int sub = warp & 3;
+    if (!skip && warp >= 2 && sub * 32 < rows) {
+      // this CTA's part of a row to the row's CTA: slot `part` of its slots of
+      // `slice` rows of BN floats, 16-byte unit q of row i at q ^ (i % 8). By way of
+      // a box of 32 rows x 32 columns of its own, so that 8 lanes store a line.
+      const uint32_t box = sbase + SLOTS_BYTES + sub * 4096;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < BN; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(tmem + (static_cast<uint32_t>(sub * 32) << 16) + c, r);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          st_shared_v4(box + lane * 128 + 16 * (q ^ (lane & 7)), r[4 * q], r[4 * q + 1],
+                       r[4 * q + 2], r[4 * q + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int l = 4 * j + (lane >> 3), q = lane & 7, in_tile = sub * 32 + l;
+          if (in_tile < rows) {
+            const float4 v = ld_shared_v4(box + l * 128 + 16 * (q ^ (l & 7)));
+            const int owner = in_tile / slice, i = in_tile - owner * slice;
+            st_shared_cluster_v4(map_to_cta(sbase, owner) + (part * slice + i) * (BN * 4) +
+                                     16 * ((c / 4 + q) ^ (i & 7)),
+                                 __float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z),
+                                 __float_as_uint(v.w));
+          }
+        }
+        __syncwarp();  // the box is written again
+      }
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();  // every part has arrived
     if (!skip && warp >= 2) {
       const Alpha al = tensor_alpha(p.a_scale, p.b_scale);
       Fp4Tensor to{};
       if constexpr (EPI == kEpiGeluFp4) to = fp4_tensor(FMT == kFp4Nv ? p.out_scale : nullptr);
-      const int rows = min(BM, p.m - tm * BM);
-      const int r0 = rows * part / splits, r1 = rows * (part + 1) / splits;
-      const int cols = min(BN, p.n - tn * BN) / 32;
-      for (int it = threadIdx.x - 64; it < (r1 - r0) * cols; it += 128) {
-        const int in_tile = r0 + it / cols, c = it % cols * 32;
-        const int row = tm * BM + in_tile, col = tn * BN + c;
-        float4 x[8] = {};
+      const int r0 = min(rows, part * slice), mine = min(rows, r0 + slice) - r0;
+      // 8 columns at a time; lanes that share a scale block of an FP4 output stay
+      // together (n is a multiple of 32)
+      const int groups = min(BN, p.n - tn * BN) / 8;
+      for (int it = threadIdx.x - 64; it < mine * groups; it += 128) {
+        const unsigned live = __activemask();
+        const int i = it / groups, g = it - i * groups;
+        const int row = tm * BM + r0 + i, col = tn * BN + 8 * g;
+        const size_t at = static_cast<size_t>(row) * p.n + col;
+        float4 x[2] = {};
         if (EPI == kEpiGatedResidual) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            x[q] = reinterpret_cast<const float4 *>(p.resid + static_cast<size_t>(row) * p.n + col)[q];
+          x[0] = reinterpret_cast<const float4 *>(p.resid + at)[0];
+          x[1] = reinterpret_cast<const float4 *>(p.resid + at)[1];
         }
-        float sum[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) sum[i] = 0.f;
+        float sum[8] = {};
         for (int s = 0; s < splits; ++s) {
-          const uint32_t o = map_to_cta(sbase, s) + in_tile * BN * 4;
+          const uint32_t o = sbase + (s * slice + i) * (BN * 4);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 v = ld_shared_cluster_v4(o + 16 * ((c / 4 + q) ^ (in_tile & 7)));
+          for (int q = 0; q < 2; ++q) {
+            const float4 v = ld_shared_v4(o + 16 * ((2 * g + q) ^ (i & 7)));
             sum[4 * q + 0] += v.x;
             sum[4 * q + 1] += v.y;
             sum[4 * q + 2] += v.z;
             sum[4 * q + 3] += v.w;
           }
         }
-        uint32_t r[32];
+        uint32_t r[8];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(sum[i]);
-        float v[32];
-        values32<EPI>(p, al, r, col, [&](int q) { return x[q]; }, v);
-        store32<FMT, EPI>(p, to, v, row, col);
+        for (int q = 0; q < 8; ++q) r[q] = __float_as_uint(sum[q]);
+        float v[8];
+        values<EPI>(p, al, r, col, [&](int q) { return x[q]; }, v);
+        if constexpr (EPI == kEpiGatedResidual) {
+          float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
+          o[0] = make_float4(v[0], v[1], v[2], v[3]);
+          o[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else if constexpr (EPI == kEpiGeluFp4) {
+          store_fp4_by8<FMT>(p, to, v, row, col, live);
+        } else {
+          store_bf16_row<8>(static_cast<uint16_t *>(p.out) + at, v);
+        }
       }
     }
     __syncwarp();
-    tc_fence_before();
-    cluster_sync();  // no CTA leaves while another reads its shared memory
   } else {
     tc_fence_before();
     __syncthreads();
@@ -672,7 +727,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           __syncwarp();
         }
         float v[32];
-        values32<EPI>(p, al, r, col, [&](int q) { return ld_shared_v4(o + 16 * (q ^ (lane & 7))); }, v);
+        values<EPI>(p, al, r, col, [&](int q) { return ld_shared_v4(o + 16 * (q ^ (lane & 7))); }, v);
         if constexpr (EPI == kEpiGeluFp4) {
           if (row < p.m) store_fp4<FMT>(p, to, v, row, col);
         } else if constexpr (EPI == kEpiGatedResidual) {
@@ -811,24 +866,36 @@ Fp4GemmPlan fp4_gemm_plan(int fmt, Fp4GemmParams *p, int num_sms) {
   Fp4GemmPlan plan{};
   p->chunks = fp4_chunks(fmt, p->k);
   const int kblocks = (p->k + BK - 1) / BK;
+  const auto tiles = [&](int bm, int bn) {
+    p->tiles_m = (p->m + bm - 1) / bm;
+    p->tiles_n = (p->n + bn - 1) / bn;
+    return static_cast<long long>(p->tiles_m) * p->tiles_n;
+  };
   plan.splits = 1;
-  plan.pair = p->m > BM;
-  const int bm = plan.pair ? 2 * BM : BM, bn = plan.pair ? pair::BN : split::BN;
-  p->tiles_m = (p->m + bm - 1) / bm;
-  p->tiles_n = (p->n + bn - 1) / bn;
-  const long long tiles = static_cast<long long>(p->tiles_m) * p->tiles_n;
+  plan.box_a = BM;
   plan.box_b = split::BN;
   static_assert(split::BN == pair::BN / 2, "one box of W for both");
+  // 128 x 128 tiles where there is a multiprocessor for each (or no second block
+  // of rows): 512 x 2048 x 4096 9.4 against 12.2 us on pairs, 2304 x 768 x 768 6.4
+  // against 8.2. With two on some, pairs win: 2048 x 2048 x 8192 18.0 against 20.0.
+  const long long small = tiles(BM, split::BN);
+  plan.pair = p->m > BM && small > num_sms;
   if (plan.pair) {
-    plan.box_a = BM;
-    plan.grid = 2 * static_cast<int>(tiles < num_sms / 2 ? tiles : num_sms / 2);
-  } else {
-    plan.box_a = p->m < BM ? (p->m + 7) / 8 * 8 : BM;  // no rows that are not there
-    while (plan.splits < split::MAX_SPLIT && tiles * (plan.splits + 1) <= 2 * num_sms &&
-           kblocks / (plan.splits + 1) >= 2)
-      ++plan.splits;
-    plan.grid = static_cast<int>(tiles * plan.splits);
+    const long long t = tiles(2 * BM, pair::BN);
+    plan.grid = 2 * static_cast<int>(t < num_sms / 2 ? t : num_sms / 2);
+    return plan;
   }
+  if (p->m < BM) plan.box_a = (p->m + 7) / 8 * 8;  // no rows that are not there
+  // k shared by as many CTAs as have a multiprocessor, where that saves more than
+  // joining the parts costs. A k-block takes a CTA about 0.28 us; the join 2 us and
+  // 3.5 for 128 rows: 1 x 5376 x 14336 19.6 us in one part, 11.3 in three; 512 x
+  // 1024 x 14336 20.2 and 14.0 in four; 128 x 5376 x 5376 11.4 and 12.0 in three.
+  int parts = static_cast<int>(num_sms / small);
+  if (parts > split::MAX_SPLIT) parts = split::MAX_SPLIT;
+  if (parts > kblocks / 2) parts = kblocks / 2;
+  const int rows = p->m < BM ? p->m : BM;
+  if (parts > 1 && 0.28 * (kblocks - kblocks / parts) > 2.0 + 3.5 * rows / BM) plan.splits = parts;
+  plan.grid = static_cast<int>(small * plan.splits);
   return plan;
 }
 

@@ -167,8 +167,11 @@ def operand(fmt, rows, k, seed, exact, g=None):
 
 SHAPES = [(1, 32, 64), (1, 64, 128), (3, 96, 192), (128, 128, 256), (129, 160, 320), (200, 768, 832),
           (127, 2304, 768), (288, 2304, 768), (257, 416, 5376), (640, 1056, 448),
-          # k shared by clusters of 2 to 8 CTAs: even and uneven shares, rows fewer and more than CTAs
-          (1, 96, 5376), (3, 256, 1088), (100, 160, 7104), (17, 416, 2112), (128, 64, 4160), (7, 32, 3904)]
+          (3, 256, 1088), (17, 416, 2112), (128, 64, 4160),
+          # k shared by clusters of 3, 5, 7 and 8 CTAs: even and uneven shares, rows fewer and more than CTAs
+          (2, 5376, 3328), (9, 3200, 3328), (90, 2656, 7104), (1, 96, 5376), (100, 160, 7104), (7, 32, 3904),
+          # pairs of CTAs: ragged rows (one in the last tile, none in a pair's second CTA) and columns
+          (1300, 2112, 320), (2049, 1184, 832), (150, 9632, 192), (2304, 1376, 64)]
 
 
 @FMTS
@@ -206,7 +209,8 @@ def sum_bound(av, wv, k):
 
 @FMTS
 @pytest.mark.parametrize("gelu_tanh", [False, True], ids=["erf", "tanh"])
-@pytest.mark.parametrize("m,n,k", [(1, 64, 256), (5, 128, 704), (300, 320, 768), (385, 1024, 320)])
+@pytest.mark.parametrize("m,n,k", [(1, 64, 256), (5, 128, 704), (300, 320, 768), (385, 1024, 320), (6, 192, 6144),
+                                   (1301, 2112, 704)])
 def test_linear_epilogues(ctx, fmt, gelu_tanh, m, n, k):
     from image_generation_b200 import h3dit as H
 
