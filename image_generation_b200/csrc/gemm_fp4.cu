@@ -176,27 +176,38 @@ H3_DEV void store_fp4_by8(const Fp4GemmParams &p, const Fp4Tensor &t, const floa
 namespace split {
 constexpr int BN = 128;
 constexpr int THREADS = 192;
-constexpr int STAGES = 3;
 constexpr int MAX_SPLIT = 8;
-constexpr int A_BYTES = BM * BKB, B_BYTES = BN * BKB;
+constexpr int B_BYTES = BN * BKB;
 constexpr uint32_t TCOLS = 256;  // of each CTA's tensor memory
 constexpr uint32_t SF_COL0 = BN;
 
-template <int FMT>
+// ROWS: rows of A that are loaded, BM or, for up to 32, fewer: then a stage is
+// smaller and there is one more of them on the way. (The MMA reads BM rows of
+// shared memory; those past ROWS give rows that nobody reads.)
+template <int FMT, int ROWS>
 struct Tile {
+  static constexpr int STAGES = ROWS == BM ? 3 : 4;
+  static constexpr int A_BYTES = ROWS * BKB;
   static constexpr int SF_BYTES = Kb<FMT>::CHUNKS * SF;  // of A or W, one k-block
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 2 * SF_BYTES;
   static constexpr int NUM_BARS = 2 * STAGES + 1;
   static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + 1024 + NUM_BARS * 8 + 16;
   static constexpr uint32_t SF_COLS = 8 * Kb<FMT>::CHUNKS;  // per stage: A, then W
 };
-static_assert(SF_COL0 + STAGES * Tile<kFp4Nv>::SF_COLS <= TCOLS, "TMEM budget");
-static_assert(Tile<kFp4Nv>::STAGE_BYTES % 1024 == 0 && Tile<kFp4Mx>::STAGE_BYTES % 1024 == 0,
-              "stages start on swizzle atoms");
-static_assert(2 * (Tile<kFp4Nv>::SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
+constexpr int FEW = 32;
 constexpr int SLOTS_BYTES = (BM + MAX_SPLIT) * BN * 4;  // the parts of a slice of rows
-static_assert(SLOTS_BYTES + 4 * 4096 <= STAGES * Tile<kFp4Mx>::STAGE_BYTES,
-              "slots and boxes fit into the stages");
+template <int FMT, int ROWS>
+constexpr bool tile_ok() {
+  using T = Tile<FMT, ROWS>;
+  return SF_COL0 + T::STAGES * T::SF_COLS <= TCOLS &&       // tensor memory
+         T::STAGE_BYTES % 1024 == 0 &&                      // stages start on swizzle atoms
+         BM * BKB <= T::STAGE_BYTES &&                      // the MMA's A rows lie in the stage
+         2 * (T::SMEM_BYTES + 1024) <= 228 * 1024 &&        // two CTAs per SM
+         SLOTS_BYTES + 4 * 4096 <= T::STAGES * T::STAGE_BYTES;  // slots and boxes fit
+}
+static_assert(tile_ok<kFp4Nv, BM>() && tile_ok<kFp4Mx, BM>() && tile_ok<kFp4Nv, FEW>() &&
+                  tile_ok<kFp4Mx, FEW>(),
+              "tile sizes");
 
 // A row's 32 values to global memory.
 template <int FMT, int EPI>
@@ -214,13 +225,14 @@ H3_DEV void store32(const Fp4GemmParams &p, const Fp4Tensor &to, const float (&v
   }
 }
 
-template <int FMT, int EPI>
+template <int FMT, int EPI, int ROWS>
 __global__ void __launch_bounds__(THREADS, 2)
     gemm_fp4_split(const __grid_constant__ CUtensorMap tma_a,
                    const __grid_constant__ CUtensorMap tma_b, const Fp4GemmParams p, int splits,
                    int a_rows) {
-  using T = Tile<FMT>;
+  using T = Tile<FMT, ROWS>;
   constexpr bool NV = FMT == kFp4Nv;
+  constexpr int STAGES = T::STAGES, A_BYTES = T::A_BYTES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -464,16 +476,17 @@ __global__ void __launch_bounds__(THREADS, 2)
   }
 }
 
-template <int FMT, int EPI>
-cudaError_t launch(const Fp4GemmMaps &t, const Fp4GemmParams &p, const Fp4GemmPlan &plan,
-                   cudaStream_t s) {
+template <int FMT, int EPI, int ROWS>
+cudaError_t launch_tile(const Fp4GemmMaps &t, const Fp4GemmParams &p, const Fp4GemmPlan &plan,
+                        cudaStream_t s) {
   static PerDevice smem_attr;
-  cudaError_t e = set_smem_once(smem_attr, gemm_fp4_split<FMT, EPI>, Tile<FMT>::SMEM_BYTES);
+  constexpr int kSmem = Tile<FMT, ROWS>::SMEM_BYTES;
+  cudaError_t e = set_smem_once(smem_attr, gemm_fp4_split<FMT, EPI, ROWS>, kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(plan.grid, 1, 1);
   cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = Tile<FMT>::SMEM_BYTES;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -482,7 +495,15 @@ cudaError_t launch(const Fp4GemmMaps &t, const Fp4GemmParams &p, const Fp4GemmPl
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm_fp4_split<FMT, EPI>, t.a, t.b, p, plan.splits, plan.box_a);
+  return cudaLaunchKernelEx(&cfg, gemm_fp4_split<FMT, EPI, ROWS>, t.a, t.b, p, plan.splits,
+                            plan.box_a);
+}
+
+template <int FMT, int EPI>
+cudaError_t launch(const Fp4GemmMaps &t, const Fp4GemmParams &p, const Fp4GemmPlan &plan,
+                   cudaStream_t s) {
+  return plan.box_a <= FEW ? launch_tile<FMT, EPI, FEW>(t, p, plan, s)
+                           : launch_tile<FMT, EPI, BM>(t, p, plan, s);
 }
 }  // namespace split
 
