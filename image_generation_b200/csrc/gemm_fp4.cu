@@ -57,10 +57,12 @@ H3_DEV Alpha tensor_alpha(const float *ga, const float *gw) {
 // by Abramowitz & Stegun, Handbook of Mathematical Functions, 7.1.26 (|error| of
 // erf <= 1.5e-7): q = t (b1 + ... + b5 t^4) e^(-x^2 / 2), t = 1 / (1 + p |x| / sqrt 2).
 // In packed fp32 pairs: one value at a time, the epilogue of a product
-// 16896 x 14336 x 5376 took 97 of its 514 us.
+// 16896 x 14336 x 5376 took 97 of its 514 us. |x| is kept finite, so that its
+// product with an e of 0 is 0 (a NaN stays one by way of e).
 H3_DEV void gelu2(float &a, float &b) {
   auto c2 = [](float c) { return f2_pack(c, c); };
-  const uint64_t x = f2_pack(a, b), ax = f2_pack(fabsf(a), fabsf(b));
+  const uint64_t x = f2_pack(a, b);
+  const uint64_t ax = f2_pack(fminf(fabsf(a), 3e38f), fminf(fabsf(b), 3e38f));
   float d0, d1, t0, t1, e0, e1;
   f2_unpack(f2_fma(ax, c2(0.3275911f * 0.70710678118654752f), c2(1.f)), d0, d1);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t0) : "f"(d0));

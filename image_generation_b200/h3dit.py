@@ -592,6 +592,8 @@ class Context:
             raise _bad(f"the context lives on cuda:{index}, the current device is "
                        f"cuda:{torch.cuda.current_device()}")
         if stream is not None:
+            if stream.device.index != index:
+                raise _bad(f"the stream is on {stream.device}, the context on cuda:{index}")
             return stream.cuda_stream
         return torch._C._cuda_getCurrentRawStream(index)  # current_stream() without its object
 

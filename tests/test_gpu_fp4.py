@@ -322,6 +322,69 @@ def test_nan_scales_reach_their_rows_only(ctx, fmt):
     assert np.array_equal(got[keep], ref[keep])
 
 
+@pytest.mark.parametrize("m", [3, 1300], ids=["few_rows", "pairs"])
+def test_sums_past_fp32_and_their_gelu(ctx, m):
+    """Scales so large that sums leave fp32: infinities as fp32 has them, GELU of
+    plus infinity is itself and of minus infinity 0, other rows as ever."""
+    from image_generation_b200 import h3dit as H
+
+    n, k = 2112, 128
+    codes = np.full((m, k), 2, np.uint8)                  # ones
+    byte = np.full((m, k // 32), 127, np.uint8)
+    byte[1], byte[2] = 250, 250
+    codes[2] = 10                                         # minus ones
+    w = dev(R.pack(np.full((n, k), 2, np.uint8)))
+    wsf = dev(R.sf_layout(np.full((n, k // 32), 135, np.uint8)))
+    a, asf = dev(R.pack(codes)), dev(R.sf_layout(byte))
+    for epi, want in ((H.H3DIT_EPI_STORE, [np.inf, -np.inf]), (H.H3DIT_EPI_GELU, [np.inf, 0.0])):
+        out = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+        ctx.linear_fp4(R.MX, epi, a, asf, w, wsf, out)
+        ok(ctx)
+        got = to_np(out)
+        assert np.all(got[0] == 32768) and np.all(got[3:] == 32768)
+        assert np.all(got[1] == want[0]) and np.all(got[2] == want[1])
+
+
+def test_offsets_past_31_bits(ctx):
+    """More than 2^31 elements in and out: the last rows as when they come alone."""
+    from image_generation_b200 import h3dit as H
+
+    rows, k, last = 430_080, 5056, 200                    # 2.17e9 elements
+    x = torch.empty(rows, k, dtype=torch.bfloat16, device="cuda").normal_()
+    q = torch.empty(rows, k // 2, dtype=torch.uint8, device="cuda")
+    sf = torch.empty(R.sf_bytes(R.NV, rows, k), dtype=torch.uint8, device="cuda")
+    t = torch.full((1,), 6.0 / 2688, device="cuda")
+    ctx.fp4_quantize(R.NV, x, q, sf, tensor_scale=t)
+    out = torch.empty_like(x)
+    ctx.fp4_dequantize(R.NV, q, sf, out, tensor_scale=t)
+    alone = x[-last:].clone()
+    q1 = torch.empty(last, k // 2, dtype=torch.uint8, device="cuda")
+    sf1 = torch.empty(R.sf_bytes(R.NV, last, k), dtype=torch.uint8, device="cuda")
+    o1 = torch.empty_like(alone)
+    ctx.fp4_quantize(R.NV, alone, q1, sf1, tensor_scale=t)
+    ctx.fp4_dequantize(R.NV, q1, sf1, o1, tensor_scale=t)
+    ok(ctx)
+    assert torch.equal(q[-last:], q1) and torch.equal(out[-last:], o1)
+    amax, want = torch.empty(1, device="cuda"), x.abs().max().float() / 2688
+    x[-1, -1] = 2 * x.abs().max()
+    ctx.fp4_tensor_scale(x, amax)
+    assert amax.item() == (2 * want).item()
+    del x, out
+    # the product: 430080 x 5056 outputs; codes of a k of 64
+    a = q.view(-1)[: rows * 32].view(rows, 32)
+    w, wsf, _ = operand(R.NV, 5056, 64, 3, True)
+    asf = torch.full((R.sf_bytes(R.NV, rows, 64),), 0x38, dtype=torch.uint8, device="cuda")
+    for epi, dt in ((H.H3DIT_EPI_STORE, torch.bfloat16), (H.H3DIT_EPI_GATED_RESIDUAL, torch.float32)):
+        kw = {} if dt == torch.bfloat16 else dict(gate=torch.ones(5056, device="cuda"))
+        big = torch.ones(rows, 5056, dtype=dt, device="cuda")
+        small = torch.ones(last, 5056, dtype=dt, device="cuda")
+        ctx.linear_fp4(R.NV, epi, a, asf, w, wsf, big, **kw)
+        ctx.linear_fp4(R.NV, epi, a[-last:].clone(), asf[: R.sf_bytes(R.NV, last, 64)].clone(), w, wsf, small, **kw)
+        ok(ctx)
+        assert torch.equal(big[-last:], small)
+        del big
+
+
 def test_graph_replay_and_side_stream(ctx):
     from image_generation_b200 import h3dit as H
 

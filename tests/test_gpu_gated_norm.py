@@ -191,6 +191,21 @@ def test_more_rows_than_ctas_match_alone(ctxs):
         assert torch.equal(xo1[0], xo[row]) and torch.equal(out1[0], out[row])
 
 
+def test_offsets_past_31_bits(ctxs):
+    n, d = 262_200, 8192                                  # 2.15e9 elements
+    ctx = ctx_for(ctxs, d)
+    x = torch.empty(n, d, device="cuda").normal_()
+    y = torch.empty(n, d, dtype=torch.bfloat16, device="cuda").normal_()
+    out = torch.empty(n, d, dtype=torch.bfloat16, device="cuda")
+    x1, y1 = x[-3:].clone(), y[-3:].clone()
+    o1 = torch.empty(3, d, dtype=torch.bfloat16, device="cuda")
+    g = torch.randn(d, device="cuda")
+    for a, b, o in ((x, y, out), (x1, y1, o1)):
+        ctx.gated_norm(a, a, 0, o, branch=b, gate=g, post_norm=True)
+    ok(ctx)
+    assert torch.equal(x[-3:], x1) and torch.equal(out[-3:], o1)
+
+
 def test_refusals(ctxs):
     from image_generation_b200 import h3dit as H
 

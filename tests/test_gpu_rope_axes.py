@@ -175,6 +175,20 @@ def test_zero_and_extreme_heads(ctx):
     assert np.all(np.abs(got - ref)[fin] <= bound(ref, size, True, True)[fin])
 
 
+def test_offsets_past_31_bits(ctx):
+    from image_generation_b200 import h3dit as H
+
+    n, h, dh = 300_100, 56, 128                           # 2.15e9 elements, in place
+    spec = H.make_rope_spec(dh, (16, 24, 24))
+    x = torch.empty(n, h * dh, dtype=torch.bfloat16, device="cuda").normal_()
+    pos = dev(positions(n, 2))
+    x1 = x[-5:].clone()
+    ctx.rope_axes(spec, pos, x, x, h)
+    ctx.rope_axes(spec, pos[-5:].clone(), x1, x1, h)
+    ok(ctx)
+    assert torch.equal(x[-5:], x1)
+
+
 def test_refusals(ctx):
     from image_generation_b200 import h3dit as H
 
