@@ -303,10 +303,9 @@ def _bad(msg: str) -> "H3DitError":
     return H3DitError(H3DIT_ERR_INVALID_ARG, msg)
 
 
-def _arg(dev, t, what: str, dtypes, shape=None, dense: bool = True) -> int | None:
+def _arg(dev, t, what: str, dtypes, shape=None) -> int | None:
     """Device address of an argument of the FP4, norm and rotary calls: on the
-    context's device, of one of `dtypes`, of `shape`, and contiguous (dense) or
-    with contiguous rows that do not overlap."""
+    context's device, of one of `dtypes`, of `shape`, and contiguous."""
     if t is None:
         return None
     # the usual case in as few calls as can be: small launches wait for this
@@ -319,13 +318,29 @@ def _arg(dev, t, what: str, dtypes, shape=None, dense: bool = True) -> int | Non
         raise _bad(f"{what} has dtype {t.dtype}")
     if shape is not None and t.shape != shape:
         raise _bad(f"{what} has shape {tuple(t.shape)}, not {shape}")
-    if dense:
-        if not t.is_contiguous():
-            raise _bad(f"{what} is not contiguous")
-    elif t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (
-            t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        raise _bad(f"{what} needs rows of consecutive elements that do not overlap")
+    if not t.is_contiguous():
+        raise _bad(f"{what} is not contiguous")
     return t.data_ptr()
+
+
+def _rows(dev, t, what: str, dtypes, shape) -> Tuple[int, int]:
+    """Address and row stride of a matrix whose rows may lie apart."""
+    if t.dtype in dtypes and t.get_device() == dev.index and t.shape == shape:
+        ld, one = t.stride()
+        if one == 1 and shape[0] > 1 and ld >= shape[1]:
+            return t.data_ptr(), ld
+        if one == 1 and shape[0] == 1:
+            return t.data_ptr(), (shape[1] + 7) // 8 * 8
+    if t.device != dev:
+        raise _bad(f"{what} is on {t.device}, the context on {dev}")
+    if t.dtype not in dtypes:
+        raise _bad(f"{what} has dtype {t.dtype}")
+    if t.shape != shape:
+        raise _bad(f"{what} has shape {tuple(t.shape)}, not {shape}")
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise _bad(f"{what} needs rows of consecutive elements that do not overlap")
+    # the stride of a single row is nobody's: one that the alignment rules take
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
 
 
 def _matrix(t, what: str) -> Tuple[int, int]:
@@ -334,11 +349,6 @@ def _matrix(t, what: str) -> Tuple[int, int]:
     if t.dim() != 2:
         raise _bad(f"{what} has shape {tuple(t.shape)}, not [rows, columns]")
     return t.shape
-
-
-def _ld(t, width: int) -> int:
-    """Row stride of a matrix of rows (torch leaves it open for one row)."""
-    return t.stride(0) if t.shape[0] > 1 else max(width, (width + 7) // 8 * 8)
 
 
 def ipc_handle(t) -> Tuple[bytes, int]:
@@ -624,9 +634,9 @@ class Context:
     def _fp4_source(self, src) -> tuple:
         import torch
 
-        rows, k = _matrix(src, "src")
-        ptr = _arg(self.workspace.device, src, "src", (torch.bfloat16, torch.float32), None, False)
-        return ptr, int(src.dtype == torch.float32), _ld(src, k), rows, k
+        shape = rows, k = _matrix(src, "src")
+        ptr, ld = _rows(self.workspace.device, src, "src", (torch.bfloat16, torch.float32), shape)
+        return ptr, src.dtype == torch.float32, ld, rows, k
 
     def fp4_tensor_scale(self, src, scale_out, stream=None) -> None:
         """scale_out (one fp32) = src's largest finite magnitude over 2688 (1 if
@@ -684,28 +694,22 @@ class Context:
             _arg(dev, gate, "gate", f32, (n,)), _arg(dev, resid, "resid", f32, (m, n)),
             self._here(stream)))
 
-    def _modulation(self, parts, groups: int) -> tuple:
-        """Addresses and the common row stride of gate, shift and scale."""
+    def _modulation(self, name: str, t, groups: int) -> Tuple[int | None, int]:
+        """Address and row stride of gate, shift or scale."""
+        if t is None:
+            return None, 0
         import torch
 
         dev, f32, D = self.workspace.device, (torch.float32,), self.cfg.hidden
-        ptrs, ld = [], None
-        for name, t in parts:
-            if t is None:
-                ptrs.append(None)
-            elif t.dim() == 1:
-                if groups > 1:
-                    raise _bad(f"{name} has one row for {groups} groups")
-                ptrs.append(_arg(dev, t, name, f32, (D,)))
-            else:
-                if t.shape[0] < groups:
-                    raise _bad(f"{name} has {t.shape[0]} rows for {groups} groups")
-                ptrs.append(_arg(dev, t, name, f32, (t.shape[0], D), False))
-                if groups > 1:
-                    if ld is not None and ld != t.stride(0):
-                        raise _bad("gate, shift and scale need equal row strides")
-                    ld = t.stride(0)
-        return ptrs, ld or 0
+        if t.dim() == 1:
+            if groups > 1:
+                raise _bad(f"{name} has one row for {groups} groups")
+            return _arg(dev, t, name, f32, (D,)), 0
+        rows = _matrix(t, name)[0]
+        if rows < groups:
+            raise _bad(f"{name} has {rows} rows for {groups} groups")
+        ptr, ld = _rows(dev, t, name, f32, (rows, D))
+        return ptr, ld if groups > 1 else 0
 
     def gated_norm(self, x, x_out, out_kind: int, out, out_sf=None, out_scale=None, branch=None,
                    gate=None, shift=None, scale=None, rows_per_group: int = 0,
@@ -726,7 +730,13 @@ class Context:
         rows = (n, D)
         xp = _arg(dev, x, "x", f32, rows)
         groups = -(-n // rows_per_group) if rows_per_group > 0 else 1
-        mods, ld = self._modulation((("gate", gate), ("shift", shift), ("scale", scale)), groups)
+        gate, ld = self._modulation("gate", gate, groups)
+        shift, ld1 = self._modulation("shift", shift, groups)
+        scale, ld2 = self._modulation("scale", scale, groups)
+        if groups > 1:
+            ld = ld or ld1 or ld2
+            if (ld1 and ld1 != ld) or (ld2 and ld2 != ld):
+                raise _bad("gate, shift and scale need equal row strides")
         if out_kind == H3DIT_NORM_OUT_BF16:
             op = _arg(dev, out, "out", (torch.bfloat16,), rows)
             sp = _arg(dev, out_sf, "out_sf", (torch.uint8,))
@@ -743,8 +753,8 @@ class Context:
             _arg(dev, branch, "branch", (torch.bfloat16, torch.float32), rows),
             branch is not None and branch.dtype == torch.float32, bool(post_norm),
             _arg(dev, post_weight, "post_weight", f32, (D,)),
-            _arg(dev, pre_weight, "pre_weight", f32, (D,)), *mods, ld, n, rows_per_group,
-            residual_scale, out_kind, op, sp, self._scalar(out_scale, "out_scale"))
+            _arg(dev, pre_weight, "pre_weight", f32, (D,)), gate, shift, scale, ld, n,
+            rows_per_group, residual_scale, out_kind, op, sp, self._scalar(out_scale, "out_scale"))
         self._check(lib.h3dit_gated_norm(self.handle, C.byref(args), self._here(stream)))
 
     def rope_axes(self, spec: h3dit_rope_spec, positions, q, q_out, heads_q: int, k=None,
@@ -766,8 +776,8 @@ class Context:
                 raise _bad(f"{name} and {name}_out are needed")
             dt = dt or t.dtype
             types, shape = (dt,) if dt in (torch.bfloat16, torch.float32) else (), (n, heads * dh)
-            sides += (_arg(dev, t, name, types, shape, False), _ld(t, shape[1]),
-                      _arg(dev, o, name + "_out", types, shape, False), _ld(o, shape[1]), heads)
+            sides += (*_rows(dev, t, name, types, shape),
+                      *_rows(dev, o, name + "_out", types, shape), heads)
         self._check(lib.h3dit_rope_axes(
             self.handle, C.byref(spec), _arg(dev, positions, "positions", f32, (n, 3)), n,
             dt == torch.float32, *sides, _arg(dev, q_weight, "q_weight", f32, (dh,)),
