@@ -117,13 +117,14 @@ H3_DEV void store_chunk(const GatedNormParams &p, const Fp4Tensor &t, int row, i
   }
 }
 
-template <typename TB, int OUT>
+// FULL: every thread has both of its chunks.
+template <typename TB, int OUT, bool FULL>
 __global__ void __launch_bounds__(kMaxThreads, 1)
     gated_norm_kernel(const GatedNormParams p, bool post, int depth) {
   extern __shared__ __align__(16) uint8_t rows_smem[];
   __shared__ __align__(16) float red[2][kMaxWarps];
   const int c0 = threadIdx.x, c1 = threadIdx.x + blockDim.x;  // chunks of this thread
-  const bool on0 = c0 < p.d / 4, on1 = c1 < p.d / 4;
+  const bool on0 = FULL || c0 < p.d / 4, on1 = FULL || c1 < p.d / 4;
   const float inv_d = 1.f / static_cast<float>(p.d);
   const TB *branch = static_cast<const TB *>(p.branch);
   Fp4Tensor t{};
@@ -135,29 +136,40 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 
   const uint32_t row_bytes = p.d * (4 + sizeof(TB));
   const uint32_t rows0 = smem_u32(rows_smem);
-  // one group of copies per row, empty past the last
-  auto fetch = [&](long long row, int slot) {
-    if (row < p.n) {
-      const uint32_t at = rows0 + slot * row_bytes;
-      auto chunk = [&](int c) {
-        cp_async16(at + 16 * c, p.x + static_cast<size_t>(row) * p.d + 4 * c);
-        if (branch)
-          cp_async<4 * sizeof(TB)>(at + 4 * p.d + 4 * sizeof(TB) * c,
-                                   branch + static_cast<size_t>(row) * p.d + 4 * c);
-      };
-      if (on0) chunk(c0);
-      if (on1) chunk(c1);
+  // one group of copies per row, empty past the last: this CTA's rows in turn
+  const long long apart = static_cast<long long>(gridDim.x) * p.d;
+  const long long begin = static_cast<long long>(blockIdx.x) * p.d + 4 * c0;
+  const int second = 4 * static_cast<int>(blockDim.x);  // from a row's first chunk to its second
+  const float *next_x = p.x + begin;
+  const TB *next_y = branch ? branch + begin : nullptr;
+  long long next_row = blockIdx.x;
+  uint32_t next_at = rows0;
+  const uint32_t rows_end = rows0 + depth * row_bytes, branch_at = 4 * p.d;
+  auto fetch = [&] {
+    if (next_row < p.n) {
+      const uint32_t at = next_at + 16 * c0, by = next_at + branch_at + 4 * sizeof(TB) * c0;
+      if (on0) cp_async16(at, next_x);
+      if (on1) cp_async16(at + 4 * second, next_x + second);
+      if (branch) {
+        if (on0) cp_async<4 * sizeof(TB)>(by, next_y);
+        if (on1) cp_async<4 * sizeof(TB)>(by + sizeof(TB) * second, next_y + second);
+      }
     }
     cp_async_commit();
+    next_row += gridDim.x;
+    next_x += apart;
+    if (branch) next_y += apart;
+    next_at += row_bytes;
+    if (next_at == rows_end) next_at = rows0;
   };
-  for (int i = 0; i < depth - 1; ++i)
-    fetch(blockIdx.x + static_cast<long long>(i) * gridDim.x, i);
+  for (int i = 0; i < depth - 1; ++i) fetch();
 
   // gate post_weight, pre_weight (1 + scale), shift of the columns of this thread
   Four gw[2] = {all(0.f), all(0.f)}, up[2] = {all(0.f), all(0.f)}, add[2] = {all(0.f), all(0.f)};
   const Four rs = all(p.residual_scale);
   long long group_end = 0;  // first row past the modulation in hand
-  int slot = 0;
+  uint32_t at = rows0;
+  float4 *x_out = p.x_out ? reinterpret_cast<float4 *>(p.x_out + begin) : nullptr;
   for (int row = blockIdx.x; row < p.n; row += gridDim.x) {
     if (row >= group_end) {
       const int g = row / p.rows_per_group;
@@ -174,18 +186,19 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
       if (on0) load(0, c0);
       if (on1) load(1, c1);
     }
-    // the slot that the row before this one left
-    fetch(row + static_cast<long long>(depth - 1) * gridDim.x, slot == 0 ? depth - 1 : slot - 1);
+    fetch();  // to the slot that the row before this one left
     cp_async_wait_but(depth - 1);
-    Four x[2] = {all(0.f), all(0.f)}, y[2] = {all(0.f), all(0.f)};
+    Four x[2], y[2] = {all(0.f), all(0.f)};
+    if (!FULL) x[0] = x[1] = all(0.f);
     {
-      const uint32_t at = rows0 + slot * row_bytes, by = at + 4 * p.d;
-      if (on0) x[0] = chunk4(at + 16 * c0, p.x);
-      if (on1) x[1] = chunk4(at + 16 * c1, p.x);
-      if (branch && on0) y[0] = chunk4(by + 4 * sizeof(TB) * c0, branch);
-      if (branch && on1) y[1] = chunk4(by + 4 * sizeof(TB) * c1, branch);
+      const uint32_t ax = at + 16 * c0, ay = at + branch_at + 4 * sizeof(TB) * c0;
+      if (on0) x[0] = chunk4(ax, p.x);
+      if (on1) x[1] = chunk4(ax + 4 * second, p.x);
+      if (branch && on0) y[0] = chunk4(ay, branch);
+      if (branch && on1) y[1] = chunk4(ay + sizeof(TB) * second, branch);
     }
-    if (++slot == depth) slot = 0;
+    at += row_bytes;
+    if (at == rows_end) at = rows0;
     if (post) {
       const Four r = all(rsqrtf(block_sum(sum_squares(y[0], y[1]), red[0]) * inv_d + p.eps));
       y[0] = mul(y[0], r);
@@ -194,10 +207,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     // without a branch y is 0
     x[0] = fma(gw[0], y[0], mul(x[0], rs));
     x[1] = fma(gw[1], y[1], mul(x[1], rs));
-    if (p.x_out) {
-      float4 *o = reinterpret_cast<float4 *>(p.x_out + static_cast<size_t>(row) * p.d);
-      if (on0) __stcs(o + c0, unpack(x[0]));
-      if (on1) __stcs(o + c1, unpack(x[1]));
+    if (x_out) {
+      if (on0) __stcs(x_out, unpack(x[0]));
+      if (on1) __stcs(x_out + blockDim.x, unpack(x[1]));
+      x_out += apart / 4;
     }
     const Four r = all(rsqrtf(block_sum(sum_squares(x[0], x[1]), red[1]) * inv_d + p.eps));
     store_chunk<OUT>(p, t, row, c0, on0, fma(mul(x[0], r), up[0], add[0]));
@@ -207,8 +220,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   cp_async_wait_all();
 }
 
-template <typename TB, int OUT>
-cudaError_t launch(const GatedNormParams &p, bool post, int num_sms, cudaStream_t s) {
+template <typename TB, int OUT, bool FULL>
+cudaError_t launch_full(const GatedNormParams &p, bool post, int num_sms, cudaStream_t s) {
   static PerDevice attr;
   const int threads = (p.d / 8 + 31) / 32 * 32;
   const int row_bytes = p.d * (4 + static_cast<int>(sizeof(TB)));
@@ -220,11 +233,17 @@ cudaError_t launch(const GatedNormParams &p, bool post, int num_sms, cudaStream_
   if (depth < 2) depth = 2;
   const long long most = static_cast<long long>(num_sms) * per_sm;
   if (p.n <= most) depth = 2;  // a CTA has one row
-  cudaError_t e = set_smem_once(attr, gated_norm_kernel<TB, OUT>, kSmemBytes);
+  cudaError_t e = set_smem_once(attr, gated_norm_kernel<TB, OUT, FULL>, kSmemBytes);
   if (e != cudaSuccess) return e;
   const int grid = static_cast<int>(p.n < most ? p.n : most);
-  gated_norm_kernel<TB, OUT><<<grid, threads, depth * row_bytes, s>>>(p, post, depth);
+  gated_norm_kernel<TB, OUT, FULL><<<grid, threads, depth * row_bytes, s>>>(p, post, depth);
   return cudaGetLastError();
+}
+
+template <typename TB, int OUT>
+cudaError_t launch(const GatedNormParams &p, bool post, int num_sms, cudaStream_t s) {
+  return p.d % 256 == 0 ? launch_full<TB, OUT, true>(p, post, num_sms, s)
+                        : launch_full<TB, OUT, false>(p, post, num_sms, s);
 }
 
 template <typename TB>
