@@ -217,9 +217,9 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-int grid_for(long long units, int num_sms) {
-  const long long want = (units + kThreads - 1) / kThreads;
-  return static_cast<int>(want < 8LL * num_sms ? want : 8LL * num_sms);
+int grid_for(long long units, int num_sms, int per_sm) {
+  const long long want = (units + kThreads - 1) / kThreads, most = static_cast<long long>(per_sm) * num_sms;
+  return static_cast<int>(want < most ? want : most);
 }
 
 }  // namespace
@@ -228,7 +228,7 @@ cudaError_t launch_fp4_quantize(int fmt, const void *src, bool f32, long long ld
                                 const float *g, uint8_t *dst, uint8_t *sf, int num_sms,
                                 cudaStream_t s) {
   const long long units = static_cast<long long>(rows) * (k / 16);
-  const int grid = grid_for(units, num_sms);
+  const int grid = grid_for(units, num_sms, 8);
   const bool wide = is_wide(src, ld * (f32 ? 4 : 2));
   auto run = [&](auto kernel, auto *p) {
     kernel<<<grid, kThreads, 0, s>>>(p, ld, wide, rows, k, g, dst, sf);
@@ -246,7 +246,8 @@ cudaError_t launch_fp4_quantize(int fmt, const void *src, bool f32, long long ld
 cudaError_t launch_fp4_dequantize(int fmt, const uint8_t *q, const uint8_t *sf, int rows, int k,
                                   const float *g, void *out, int num_sms, cudaStream_t s) {
   const long long units = static_cast<long long>(rows) * (k / 16);
-  const int grid = grid_for(units, num_sms);
+  // more CTAs than fit at once: 38.3 against 45.9 us with 8 per SM (16896 x 5376)
+  const int grid = grid_for(units, num_sms, 64);
   uint16_t *o = static_cast<uint16_t *>(out);
   const bool wide = is_wide(out, 2LL * k);
   if (fmt == kFp4Mx)
@@ -260,7 +261,7 @@ cudaError_t launch_fp4_tensor_scale(const void *src, bool f32, long long ld, int
                                     float *part, unsigned *done, float *out, int num_sms,
                                     cudaStream_t s) {
   const long long units = static_cast<long long>(rows) * (k / 16);
-  int grid = grid_for(units, num_sms);
+  int grid = grid_for(units, num_sms, 8);
   if (grid > kFp4ScaleParts) grid = kFp4ScaleParts;
   const bool wide = is_wide(src, ld * (f32 ? 4 : 2));
   if (f32)

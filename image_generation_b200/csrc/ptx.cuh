@@ -212,6 +212,10 @@ H3_DEV void cp_async_wait_but(int n) {
   else
     asm volatile("cp.async.wait_group 1;" ::: "memory");
 }
+template <int N>
+H3_DEV void cp_async_wait_but() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 H3_DEV void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // ---------------------------------------------------------------- tcgen05

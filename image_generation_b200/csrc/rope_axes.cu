@@ -123,7 +123,8 @@ H3_DEV void store_pairs(const RopeAxesParams &p, T *h, int u, int lo, int hi, co
   }
 }
 
-template <typename T, int ORDER, int G_LOG2>
+// PARTIAL: part of the head passes through.
+template <typename T, int ORDER, int G_LOG2, bool PARTIAL>
 __global__ void __launch_bounds__(kThreads, kPerSm)
     rope_axes_kernel(const __grid_constant__ RopeAxesParams p, int parts) {
   __shared__ __align__(16) float cs[kThreads / 32][2][kRopeMaxPairs];  // of each warp's token
@@ -147,146 +148,168 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   const uint32_t head_at = group * p.head_dim * sizeof(T);
   const int round_units = stride * static_cast<int>(sizeof(T)) / 16;  // 16-byte pieces
   const long long tasks = static_cast<long long>(p.n) * parts;
-  for (long long task = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp; task < tasks;
-       task += static_cast<long long>(gridDim.x) * (kThreads / 32)) {
-    const long long t = task / parts;
-    const int part = static_cast<int>(task - t * parts);
-    __syncwarp();  // cs[] of the token before has been read
-    for (int pair = lane; pair < half; pair += 32) {
-      float c = 1.f, s = 0.f;  // where nothing turns
-      if (pair < turning) {
-        const int axis = pair < p.sec[0] ? 0 : pair < p.sec[0] + p.sec[1] ? 1 : 2;
-        // in half turns, reduced to [-1, 1] where fp32 is exact enough
-        double a = static_cast<double>(__ldg(p.pos + 3 * t + axis)) * p.half_turns[pair];
-        a -= 2.0 * rint(0.5 * a);
-        sincospif(static_cast<float>(a), &s, &c);
-        if (p.inverse) s = -s;
-      }
-      cs[warp][0][pair] = c;
-      cs[warp][1][pair] = s;
+  const long long task = static_cast<long long>(blockIdx.x) * (kThreads / 32) + warp;
+  if (task >= tasks) return;
+  const long long t = task / parts;
+  const int part = static_cast<int>(task - t * parts);
+  for (int pair = lane; pair < half; pair += 32) {
+    float c = 1.f, s = 0.f;  // where nothing turns
+    if (pair < turning) {
+      const int axis = pair < p.sec[0] ? 0 : pair < p.sec[0] + p.sec[1] ? 1 : 2;
+      // in half turns, reduced to [-1, 1] where fp32 is exact enough
+      double a = static_cast<double>(__ldg(p.pos + 3 * t + axis)) * p.half_turns[pair];
+      a -= 2.0 * rint(0.5 * a);
+      sincospif(static_cast<float>(a), &s, &c);
+      if (p.inverse) s = -s;
     }
-    __syncwarp();
+    cs[warp][0][pair] = c;
+    cs[warp][1][pair] = s;
+  }
+  __syncwarp();
 #pragma unroll 1
-    for (int w = 0; w < 2; ++w) {
-      // this part's share of the heads, in rounds of GROUPS
-      const int heads = w ? p.heads[1] : p.heads[0];
-      const int rounds = (heads + GROUPS - 1) / GROUPS;
-      const int r0 = rounds * part / parts, r1 = rounds * (part + 1) / parts;
-      if (r0 >= r1) continue;
-      int head = r0 * GROUPS + group;  // of this lane in the round at hand
-      const int last = min(r1 * GROUPS, heads);
-      const int end = on ? last : 0;
-      const T *src = w ? static_cast<const T *>(p.src[1]) + t * p.ld_src[1]
-                       : static_cast<const T *>(p.src[0]) + t * p.ld_src[0];
-      T *dst = w ? static_cast<T *>(p.dst[1]) + t * p.ld_dst[1]
-                 : static_cast<T *>(p.dst[0]) + t * p.ld_dst[0];
-      dst += head * p.head_dim;
-      // rounds on their way to shared memory, whole lines at a time
-      const uint8_t *from = reinterpret_cast<const uint8_t *>(src + r0 * stride) + 16 * lane;
-      int left = (last - r0 * GROUPS) * p.head_dim * static_cast<int>(sizeof(T)) / 16 - lane;
-      uint32_t to = ring;
-      auto fetch = [&] {
+  for (int w = 0; w < 2; ++w) {
+    // this part's share of the heads, in rounds of GROUPS
+    const int heads = w ? p.heads[1] : p.heads[0];
+    const int rounds = (heads + GROUPS - 1) / GROUPS;
+    const int r0 = rounds * part / parts, r1 = rounds * (part + 1) / parts;
+    if (r0 >= r1) continue;
+    int head = r0 * GROUPS + group;  // of this lane in the round at hand
+    const int last = min(r1 * GROUPS, heads);
+    const int end = on ? last : 0;
+    const T *src = w ? static_cast<const T *>(p.src[1]) + t * p.ld_src[1]
+                     : static_cast<const T *>(p.src[0]) + t * p.ld_src[0];
+    T *dst = w ? static_cast<T *>(p.dst[1]) + t * p.ld_dst[1]
+               : static_cast<T *>(p.dst[0]) + t * p.ld_dst[0];
+    dst += head * p.head_dim;
+    // rounds on their way to shared memory, whole lines at a time
+    const uint8_t *from = reinterpret_cast<const uint8_t *>(src + r0 * stride) + 16 * lane;
+    int left = (last - r0 * GROUPS) * p.head_dim * static_cast<int>(sizeof(T)) / 16 - lane;
+    uint32_t to = ring;
+    auto fetch = [&] {
 #pragma unroll
-        for (int i = 0; i < static_cast<int>(ROUND / 512); ++i)
-          if (32 * i + lane < round_units && 32 * i < left)
-            cp_async16(to + 16 * lane + 512 * i, from + 512 * i);
-        cp_async_commit();
-        from += stride * sizeof(T);
-        left -= round_units;
-        to = to == ring + (kDepth - 1) * ROUND ? ring : to + ROUND;
-      };
-      __syncwarp();  // the ring has been read
+      for (int i = 0; i < static_cast<int>(ROUND / 512); ++i)
+        if (32 * i + lane < round_units && 32 * i < left)
+          cp_async16(to + 16 * lane + 512 * i, from + 512 * i);
+      cp_async_commit();
+      from += stride * sizeof(T);
+      left -= round_units;
+      to = to == ring + (kDepth - 1) * ROUND ? ring : to + ROUND;
+    };
+    __syncwarp();  // the ring has been read
 #pragma unroll
-      for (int i = 0; i < kDepth - 1; ++i) fetch();
-      // x = a (wa c) - b (wb s), y = b (wb c) + a (wa s)
-      Eight ac = shared8(&cs[warp][0][on ? 8 * u : 0]), as = shared8(&cs[warp][1][on ? 8 * u : 0]);
-      Eight bc = ac, bs = as;
-      if (const float *weight = w ? p.weight[1] : p.weight[0]; weight && on) {
-        float wa[8], wb[8];
+    for (int i = 0; i < kDepth - 1; ++i) fetch();
+    // x = a (wa c) - b (wb s), y = b (wb c) + a (wa s)
+    Eight ac = shared8(&cs[warp][0][on ? 8 * u : 0]), as = shared8(&cs[warp][1][on ? 8 * u : 0]);
+    Eight bc = ac, bs = as;
+    if (const float *weight = w ? p.weight[1] : p.weight[0]; weight && on) {
+      float wa[8], wb[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          Pair q{16 * u + 2 * i, 16 * u + 2 * i + 1};
-          if (ORDER == kSplit8) q = {lo + i, hi + i};
-          if (ORDER == kSplitAny) q = split_pair(p, 8 * u + i);
-          wa[i] = __ldg(weight + q.lo);
-          wb[i] = __ldg(weight + q.hi);
+      for (int i = 0; i < 8; ++i) {
+        Pair q{16 * u + 2 * i, 16 * u + 2 * i + 1};
+        if (ORDER == kSplit8) q = {lo + i, hi + i};
+        if (ORDER == kSplitAny) q = split_pair(p, 8 * u + i);
+        wa[i] = __ldg(weight + q.lo);
+        wb[i] = __ldg(weight + q.hi);
+      }
+      const Eight va = eight(wa), vb = eight(wb);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ac.v[i] = f2_mul(ac.v[i], va.v[i]);
+        as.v[i] = f2_mul(as.v[i], va.v[i]);
+        bc.v[i] = f2_mul(bc.v[i], vb.v[i]);
+        bs.v[i] = f2_mul(bs.v[i], vb.v[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) bs.v[i] = f2_mul(bs.v[i], f2_pack(-1.f, -1.f));
+    uint32_t at = ring;
+#pragma unroll 1
+    for (int r = r0; r < r1; ++r) {
+      __syncwarp();  // the round before has been read: its place is free
+      fetch();
+      cp_async_wait_but<kDepth - 1>();
+      __syncwarp();  // the other lanes' copies too
+      const bool live = head < end;
+      Eight a{}, b{};
+      if (live) {
+        float x[8], y[8];
+        if constexpr (ORDER == kSplitAny) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const Pair q = split_pair(p, 8 * u + i);
+            x[i] = load1(at + head_at + q.lo * sizeof(T), static_cast<const T *>(nullptr));
+            y[i] = load1(at + head_at + q.hi * sizeof(T), static_cast<const T *>(nullptr));
+          }
+        } else {
+          load8(at + head_at + lo * sizeof(T), static_cast<const T *>(nullptr), x);
+          load8(at + head_at + hi * sizeof(T), static_cast<const T *>(nullptr), y);
         }
-        const Eight va = eight(wa), vb = eight(wb);
+        pairs_of<ORDER>(x, y, a, b);
+      }
+      const uint32_t here = at + head_at;
+      at = at == ring + (kDepth - 1) * ROUND ? ring : at + ROUND;
+      float rinv = 1.f;
+      if (p.norm) {
+        uint64_t ss = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ss = f2_fma(a.v[i], a.v[i], f2_fma(b.v[i], b.v[i], ss));
+        float s0, s1;
+        f2_unpack(ss, s0, s1);
+        s0 += s1;
+#pragma unroll
+        for (int o = 1 << G_LOG2 >> 1; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
+        rinv = rsqrtf(s0 * inv_dh + p.eps);
+        const uint64_t scale = f2_pack(rinv, rinv);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          ac.v[i] = f2_mul(ac.v[i], va.v[i]);
-          as.v[i] = f2_mul(as.v[i], va.v[i]);
-          bc.v[i] = f2_mul(bc.v[i], vb.v[i]);
-          bs.v[i] = f2_mul(bs.v[i], vb.v[i]);
+          a.v[i] = f2_mul(a.v[i], scale);
+          b.v[i] = f2_mul(b.v[i], scale);
         }
       }
+      if (live) {
+        Eight x, y;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) bs.v[i] = f2_mul(bs.v[i], f2_pack(-1.f, -1.f));
-      uint32_t at = ring;
+        for (int i = 0; i < 4; ++i) {
+          x.v[i] = f2_fma(a.v[i], ac.v[i], f2_mul(b.v[i], bs.v[i]));
+          y.v[i] = f2_fma(b.v[i], bc.v[i], f2_mul(a.v[i], as.v[i]));
+        }
+        if (PARTIAL && turning < 8 * u + 8) {
+          // what passes through stays out of its neighbour, an infinity too: from the
+          // ring again, so that the others keep no registers for this
+          float fx[8], fy[8];
+          floats(x, fx);
+          floats(y, fy);
+          const float *weight = w ? p.weight[1] : p.weight[0];
 #pragma unroll 1
-      for (int r = r0; r < r1; ++r) {
-        __syncwarp();  // the round before has been read: its place is free
-        fetch();
-        cp_async_wait_but(kDepth - 1);
-        __syncwarp();  // the other lanes' copies too
-        const bool live = head < end;
-        Eight a{}, b{};
-        if (live) {
-          float x[8], y[8];
-          if constexpr (ORDER == kSplitAny) {
+          for (int i = max(0, turning - 8 * u); i < 8; ++i) {
+            Pair q{16 * u + 2 * i, 16 * u + 2 * i + 1};
+            if (ORDER != kInterleaved) q = split_pair(p, 8 * u + i);
+            const T *type = nullptr;
+            float va = load1(here + q.lo * sizeof(T), type) * rinv;
+            float vb = load1(here + q.hi * sizeof(T), type) * rinv;
+            if (weight) va *= __ldg(weight + q.lo), vb *= __ldg(weight + q.hi);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const Pair q = split_pair(p, 8 * u + i);
-              x[i] = load1(at + head_at + q.lo * sizeof(T), static_cast<const T *>(nullptr));
-              y[i] = load1(at + head_at + q.hi * sizeof(T), static_cast<const T *>(nullptr));
-            }
-          } else {
-            load8(at + head_at + lo * sizeof(T), static_cast<const T *>(nullptr), x);
-            load8(at + head_at + hi * sizeof(T), static_cast<const T *>(nullptr), y);
+            for (int j = 0; j < 8; ++j)
+              if (j == i) fx[j] = va, fy[j] = vb;
           }
-          pairs_of<ORDER>(x, y, a, b);
+          x = eight(fx);
+          y = eight(fy);
         }
-        at = at == ring + (kDepth - 1) * ROUND ? ring : at + ROUND;
-        if (p.norm) {
-          uint64_t ss = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) ss = f2_fma(a.v[i], a.v[i], f2_fma(b.v[i], b.v[i], ss));
-          float s0, s1;
-          f2_unpack(ss, s0, s1);
-          s0 += s1;
-#pragma unroll
-          for (int o = 1 << G_LOG2 >> 1; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-          s0 = rsqrtf(s0 * inv_dh + p.eps);
-          const uint64_t scale = f2_pack(s0, s0);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            a.v[i] = f2_mul(a.v[i], scale);
-            b.v[i] = f2_mul(b.v[i], scale);
-          }
-        }
-        if (live) {
-          Eight x, y;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x.v[i] = f2_fma(a.v[i], ac.v[i], f2_mul(b.v[i], bs.v[i]));
-            y.v[i] = f2_fma(b.v[i], bc.v[i], f2_mul(a.v[i], as.v[i]));
-          }
-          store_pairs<T, ORDER>(p, dst, u, lo, hi, x, y);
-        }
-        head += GROUPS;
-        dst += stride;
+        store_pairs<T, ORDER>(p, dst, u, lo, hi, x, y);
       }
+      head += GROUPS;
+      dst += stride;
     }
   }
   cp_async_wait_all();  // empty groups
 }
 
-template <typename T, int ORDER, int G_LOG2>
-cudaError_t launch_groups(const RopeAxesParams &p, int num_sms, cudaStream_t s) {
+template <typename T, int ORDER, int G_LOG2, bool PARTIAL>
+cudaError_t launch_kernel(const RopeAxesParams &p, int num_sms, cudaStream_t s) {
   static PerDevice attr;
   constexpr int kBytes = kDepth * (32 >> G_LOG2) * (16 << G_LOG2) * static_cast<int>(sizeof(T)) *
                          (kThreads / 32);
-  cudaError_t e = set_smem_once(attr, rope_axes_kernel<T, ORDER, G_LOG2>, kBytes);
+  cudaError_t e = set_smem_once(attr, rope_axes_kernel<T, ORDER, G_LOG2, PARTIAL>, kBytes);
   if (e != cudaSuccess) return e;
   const int groups = 32 >> G_LOG2;
   const int rounds = ((p.heads[0] > p.heads[1] ? p.heads[0] : p.heads[1]) + groups - 1) / groups;
@@ -294,10 +317,17 @@ cudaError_t launch_groups(const RopeAxesParams &p, int num_sms, cudaStream_t s) 
   const long long warps = static_cast<long long>(kPerSm) * num_sms * (kThreads / 32);
   long long parts = warps / p.n;
   parts = parts < 1 ? 1 : parts > rounds ? rounds : parts;
-  const long long want = (p.n * parts + kThreads / 32 - 1) / (kThreads / 32);
-  const int grid = static_cast<int>(want < kPerSm * num_sms ? want : kPerSm * num_sms);
-  rope_axes_kernel<T, ORDER, G_LOG2><<<grid, kThreads, kBytes, s>>>(p, static_cast<int>(parts));
+  // one task per warp: in persistent CTAs the last round was uneven (129 against 123 us)
+  const int grid = static_cast<int>((p.n * parts + kThreads / 32 - 1) / (kThreads / 32));
+  rope_axes_kernel<T, ORDER, G_LOG2, PARTIAL><<<grid, kThreads, kBytes, s>>>(p, static_cast<int>(parts));
   return cudaGetLastError();
+}
+
+template <typename T, int ORDER, int G_LOG2>
+cudaError_t launch_groups(const RopeAxesParams &p, int num_sms, cudaStream_t s) {
+  return 2 * (p.sec[0] + p.sec[1] + p.sec[2]) < p.head_dim
+             ? launch_kernel<T, ORDER, G_LOG2, true>(p, num_sms, s)
+             : launch_kernel<T, ORDER, G_LOG2, false>(p, num_sms, s);
 }
 
 template <typename T, int ORDER>

@@ -175,6 +175,24 @@ def test_zero_and_extreme_heads(ctx):
     assert np.all(np.abs(got - ref)[fin] <= bound(ref, size, True, True)[fin])
 
 
+@pytest.mark.parametrize("sec", [(8, 0, 24), (5, 7, 9), (0, 0, 0)])
+@pytest.mark.parametrize("inter", [False, True], ids=["split", "interleaved"])
+def test_what_passes_through_keeps_to_itself(ctx, sec, inter):
+    """Infinities and NaN in the part that does not turn come out where they went in."""
+    from image_generation_b200 import h3dit as H
+
+    n, h, dh, turning = 9, 3, 112, 2 * sum(sec)
+    x = np.random.default_rng(4).standard_normal((n, h, dh)).astype(np.float32)
+    x[2, 1, turning + 1], x[3, 0, dh - 1], x[4, 2, turning] = np.inf, np.nan, -np.inf
+    xt = dev(x.reshape(n, -1))
+    o = torch.empty_like(xt)
+    ctx.rope_axes(H.make_rope_spec(dh, sec, interleaved=inter), dev(positions(n, 1)), xt, o, h)
+    ok(ctx)
+    assert np.array_equal(to_np(o).reshape(n, h, dh)[..., turning:], x[..., turning:].astype(np.float64),
+                          equal_nan=True)
+    assert np.isfinite(to_np(o).reshape(n, h, dh)[..., :turning]).all()
+
+
 def test_offsets_past_31_bits(ctx):
     from image_generation_b200 import h3dit as H
 
