@@ -9,7 +9,9 @@
 // shuffle; four lanes (64 elements, what rows are a multiple of) join their scale
 // bytes into one store. The quantization goes from the matrix's end to its
 // beginning: what the tensor scale's pass read last is still in L2, and what it
-// writes last is what a reader from the beginning wants first. FIGURES
+// writes last is what a reader from the beginning wants first. 16896 x 5376 of
+// bf16, NVFP4: tensor scale 30 us (6.0 TB/s), quantization 42 (5.5), values 38
+// (6.1); one after another 118.
 #include "fp4.cuh"
 
 namespace h3 {
