@@ -2040,8 +2040,13 @@ h3dit_status h3dit_rope_axes(h3dit_ctx *ctx, const h3dit_rope_spec *spec, const 
   int at = 0;
   for (int i = 0; i < 3; ++i) {
     p.sec[i] = spec->sections[i];
-    for (int j = 0; j < p.sec[i]; ++j)
-      p.half_turns[at++] = std::exp(-log_theta * j / p.sec[i]) / 3.14159265358979323846;
+    const double step = std::exp(-log_theta / (p.sec[i] ? p.sec[i] : 1));
+    double w = 0.0;
+    for (int j = 0; j < p.sec[i]; ++j) {
+      // every eighth anew: seven products lose less than 1e-15
+      w = j % 8 ? w * step : std::exp(-log_theta * j / p.sec[i]) / 3.14159265358979323846;
+      p.half_turns[at++] = w;
+    }
   }
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   Launch L(ctx, H3DIT_KERNEL_ROPE_AXES, s);

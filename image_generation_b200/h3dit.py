@@ -690,8 +690,10 @@ class Context:
         self._check(lib.h3dit_linear_fp4(
             self.handle, fmt, epilogue, ap, asp, self._scalar(a_scale, "a_scale"), wp, wsp,
             self._scalar(w_scale, "w_scale"), m, n, k, op, osp,
-            self._scalar(out_scale, "out_scale"), _arg(dev, bias, "bias", f32, (n,)),
-            _arg(dev, gate, "gate", f32, (n,)), _arg(dev, resid, "resid", f32, (m, n)),
+            None if out_scale is None else self._scalar(out_scale, "out_scale"),
+            None if bias is None else _arg(dev, bias, "bias", f32, (n,)),
+            None if gate is None else _arg(dev, gate, "gate", f32, (n,)),
+            None if resid is None else _arg(dev, resid, "resid", f32, (m, n)),
             self._here(stream)))
 
     def _modulation(self, name: str, t, groups: int) -> Tuple[int | None, int]:
@@ -701,6 +703,9 @@ class Context:
         import torch
 
         dev, f32, D = self.workspace.device, (torch.float32,), self.cfg.hidden
+        if (groups == 1 and t.dtype in f32 and t.get_device() == dev.index and t.numel() == D
+                and t.shape[-1] == D and t.dim() < 3 and t.is_contiguous()):
+            return t.data_ptr(), 0
         if t.dim() == 1:
             if groups > 1:
                 raise _bad(f"{name} has one row for {groups} groups")
@@ -739,7 +744,7 @@ class Context:
                 raise _bad("gate, shift and scale need equal row strides")
         if out_kind == H3DIT_NORM_OUT_BF16:
             op = _arg(dev, out, "out", (torch.bfloat16,), rows)
-            sp = _arg(dev, out_sf, "out_sf", (torch.uint8,))
+            sp = None if out_sf is None else _arg(dev, out_sf, "out_sf", (torch.uint8,))
         elif out_kind == H3DIT_NORM_OUT_MXFP8:
             op, sp = (_arg(dev, out, "out", (torch.uint8,)),
                       _arg(dev, out_sf, "out_sf", (torch.uint8,)))
@@ -752,9 +757,10 @@ class Context:
             xp, _arg(dev, x_out, "x_out", f32, rows),
             _arg(dev, branch, "branch", (torch.bfloat16, torch.float32), rows),
             branch is not None and branch.dtype == torch.float32, bool(post_norm),
-            _arg(dev, post_weight, "post_weight", f32, (D,)),
-            _arg(dev, pre_weight, "pre_weight", f32, (D,)), gate, shift, scale, ld, n,
-            rows_per_group, residual_scale, out_kind, op, sp, self._scalar(out_scale, "out_scale"))
+            None if post_weight is None else _arg(dev, post_weight, "post_weight", f32, (D,)),
+            None if pre_weight is None else _arg(dev, pre_weight, "pre_weight", f32, (D,)),
+            gate, shift, scale, ld, n, rows_per_group, residual_scale, out_kind, op, sp,
+            None if out_scale is None else self._scalar(out_scale, "out_scale"))
         self._check(lib.h3dit_gated_norm(self.handle, C.byref(args), self._here(stream)))
 
     def rope_axes(self, spec: h3dit_rope_spec, positions, q, q_out, heads_q: int, k=None,
