@@ -149,11 +149,12 @@ H3_DEV void store_fp4(const Fp4GemmParams &p, const Fp4Tensor &t, const float (&
   }
 }
 
-// The same with 8 values in a lane: two or four neighbouring lanes (all of them
-// in `live`) share a scale block.
+// The same with 8 values in a lane: two or four neighbouring lanes share a scale
+// block, and four lanes from a multiple of four on call this together.
 template <int FMT>
 H3_DEV void store_fp4_by8(const Fp4GemmParams &p, const Fp4Tensor &t, const float (&v)[8], int row,
-                          int col, unsigned live) {
+                          int col) {
+  const unsigned live = 0xfu << (threadIdx.x & 28);
   float am = 0.f, inv;
 #pragma unroll
   for (int i = 0; i < 8; ++i) am = amax_nan(am, fabsf(v[i]));
@@ -436,7 +437,6 @@ __global__ void __launch_bounds__(THREADS, 2)
       // together (n is a multiple of 32)
       const int groups = min(BN, p.n - tn * BN) / 8;
       for (int it = threadIdx.x - 64; it < mine * groups; it += 128) {
-        const unsigned live = __activemask();
         const int i = it / groups, g = it - i * groups;
         const int row = tm * BM + r0 + i, col = tn * BN + 8 * g;
         const size_t at = static_cast<size_t>(row) * p.n + col;
@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(THREADS, 2)
           o[0] = make_float4(v[0], v[1], v[2], v[3]);
           o[1] = make_float4(v[4], v[5], v[6], v[7]);
         } else if constexpr (EPI == kEpiGeluFp4) {
-          store_fp4_by8<FMT>(p, to, v, row, col, live);
+          store_fp4_by8<FMT>(p, to, v, row, col);
         } else {
           store_bf16_row<8>(static_cast<uint16_t *>(p.out) + at, v);
         }

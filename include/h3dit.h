@@ -417,7 +417,8 @@ h3dit_status h3dit_attention_mx(h3dit_ctx *ctx, const void *q, const void *k, co
  * Q and K heads and their rotation) -> attention -> fp4_quantize -> linear_fp4
  * -> gated_norm -> linear_fp4 (GELU, FP4 rows out) -> linear_fp4.
  * These calls work on the device that was current in h3dit_create, which has to
- * be current when they are made (H3DIT_ERR_INVALID_ARG otherwise).
+ * be current when they are made (H3DIT_ERR_INVALID_ARG otherwise). An output
+ * overlaps no input unless its description allows it.
  *
  * An FP4 matrix [rows, k], k a multiple of 64, is
  *   codes   device uint8 [rows, k/2]: E2M1 (0, .5, 1, 1.5, 2, 3, 4, 6 and their
