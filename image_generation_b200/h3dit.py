@@ -696,13 +696,17 @@ class Context:
             None if resid is None else _arg(dev, resid, "resid", f32, (m, n)),
             self._here(stream)))
 
+    def _width(self) -> int:
+        """Columns of the residual stream (a decoder's config calls them width)."""
+        return self.cfg.hidden
+
     def _modulation(self, name: str, t, groups: int) -> Tuple[int | None, int]:
         """Address and row stride of gate, shift or scale."""
         if t is None:
             return None, 0
         import torch
 
-        dev, f32, D = self.workspace.device, (torch.float32,), self.cfg.hidden
+        dev, f32, D = self.workspace.device, (torch.float32,), self._width()
         if (groups == 1 and t.dtype in f32 and t.get_device() == dev.index and t.numel() == D
                 and t.shape[-1] == D and t.dim() < 3 and t.is_contiguous()):
             return t.data_ptr(), 0
@@ -726,7 +730,7 @@ class Context:
         strides for rows_per_group rows each."""
         import torch
 
-        dev, f32, D = self.workspace.device, (torch.float32,), self.cfg.hidden
+        dev, f32, D = self.workspace.device, (torch.float32,), self._width()
         n = _matrix(x, "x")[0]
         if out is None:
             raise _bad("out is needed")
@@ -877,6 +881,9 @@ class VaeDecoder(Context):
                                   _stream(stream), C.byref(handle))
         check(None, st)
         self.handle = handle
+
+    def _width(self) -> int:
+        return self.cfg.width
 
     def decode(self, latent, image, stream=None) -> None:
         """latent fp32 [C, Hl, Wl] -> image fp32 [3, 16 Hl, 16 Wl]."""

@@ -202,3 +202,47 @@ def test_block_repeats_and_replays(fmt):
     want = lib(xt)
     ok(lib.ctx)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_decoder_context_takes_the_calls():
+    """The decoder's context has them too, its width for the norm."""
+    from image_generation_b200 import h3dit as H
+    from tests.test_gpu_vae import _decoder
+
+    v = synth.VAE_SMALL
+    ctx, _ = _decoder(v, 2048)
+    n, k = 40, v.width
+    x = synth.normal_f32((n, k), 1.0, 1, "x")
+    q = torch.empty(n, k // 2, dtype=torch.uint8, device="cuda")
+    sf = torch.empty(R.sf_bytes(R.NV, n, k), dtype=torch.uint8, device="cuda")
+    t, out = torch.empty(1, device="cuda"), torch.ones(n, 32, dtype=torch.bfloat16, device="cuda")
+    ctx.gated_norm(dev(x), None, H.H3DIT_NORM_OUT_FP4_NV, q, out_sf=sf)
+    _, v64 = R.gated_norm(x)
+    ok(ctx)
+    assert_quantized(R.NV, q, sf, v64, np.float32(1))
+    ctx.fp4_tensor_scale(dev(x), t)
+    assert t.item() == float(R.tensor_scale(x))
+    w = torch.zeros(32, k // 2, dtype=torch.uint8, device="cuda")
+    wsf = torch.zeros(R.sf_bytes(R.NV, 32, k), dtype=torch.uint8, device="cuda")
+    ctx.linear_fp4(R.NV, H.H3DIT_EPI_STORE, q, sf, w, wsf, out)
+    ok(ctx)
+    assert not out.any()
+
+
+@FMTS
+def test_two_contexts_on_two_streams(fmt):
+    """Each on its own stream, their calls among one another's: as alone."""
+    w, pos, x = setup(fmt)
+    libs = [Library(fmt, w, pos) for _ in range(2)]
+    xs = [dev(x), dev(np.ascontiguousarray(x[::-1]))]
+    want = [[z.clone() for z in lib(v)] for lib, v in zip(libs, xs)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    for _ in range(5):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i] = libs[i](xs[i])
+    for i in range(2):
+        ok(libs[i].ctx)
+        assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
