@@ -1781,11 +1781,17 @@ h3dit_status run_linear_fp4(h3dit_ctx *ctx, int format, int epi, Fp4GemmParams &
   if (r == CUDA_SUCCESS) r = codes(&t.b, w, p.n, plan.box_b);
   if (r == CUDA_SUCCESS && plan.pair) r = scales(&t.a_sf, p.a_sf, p.m, 1);
   if (r == CUDA_SUCCESS && plan.pair) r = scales(&t.b_sf, p.b_sf, p.n, 2);
-  if (r == CUDA_SUCCESS && plan.pair && kernel_epi != kEpiGeluFp4) {
-    const bool f32 = kernel_epi == kEpiGatedResidual;
-    r = encode(&t.out, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-               p.out, static_cast<uint64_t>(p.n) * (f32 ? 4 : 2), f32 ? 4 : 2, p.m, f32 ? 32 : 64, 32,
-               CU_TENSOR_MAP_SWIZZLE_128B);
+  if (r == CUDA_SUCCESS && plan.pair) {
+    // the output in boxes of 32 rows x 128 bytes (FP4 rows 64)
+    if (kernel_epi == kEpiGeluFp4)
+      r = encode(&t.out, CU_TENSOR_MAP_DATA_TYPE_UINT8, p.out, p.n / 2, 1, p.m, 64, 32,
+                 CU_TENSOR_MAP_SWIZZLE_64B);
+    else if (kernel_epi == kEpiGatedResidual)
+      r = encode(&t.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p.out, 4ull * p.n, 4, p.m, 32, 32,
+                 CU_TENSOR_MAP_SWIZZLE_128B);
+    else
+      r = encode(&t.out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, p.out, 2ull * p.n, 2, p.m, 64, 32,
+                 CU_TENSOR_MAP_SWIZZLE_128B);
   }
   if (r != CUDA_SUCCESS) return ctx->fail(H3DIT_ERR_CUDA, "tensor map encode failed (%d)", (int)r);
   Launch L(ctx, H3DIT_KERNEL_LINEAR_FP4, s);

@@ -529,7 +529,7 @@ cudaError_t launch(const Fp4GemmMaps &t, const Fp4GemmParams &p, const Fp4GemmPl
 // NVFP4 two k-blocks of columns; waiting for those cost more than the pause.
 //
 // The epilogue's rows go through shared memory (boxes of 32 rows x 128 bytes per
-// warp) and leave by TMA stores.
+// warp, 64 bytes with FP4 rows) and leave by TMA stores.
 namespace pair {
 constexpr int BN = 256;
 constexpr int PARTS = 2;         // epilogue warps per TMEM lane quarter
@@ -733,6 +733,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const int row0 = (2 * tm + static_cast<int>(rank)) * BM + sub * 32;
       const int row = row0 + lane;
       const int col0 = tn * BN + 128 * part;  // this warp's 128 columns, by 32
+      uint32_t scales = 0;                    // of an FP4 output, being gathered
       // 32 columns of the warp's rows of the residual into its box, whole lines at
       // a time (a thread's own row at a time, the warps' lines did not fit into L1)
       auto fetch = [&](int j) {
@@ -758,7 +759,34 @@ __global__ void __launch_bounds__(THREADS, 1)
         float v[32];
         values<EPI>(p, al, r, col, [&](int q) { return ld_shared_v4(o + 16 * (q ^ (lane & 7))); }, v);
         if constexpr (EPI == kEpiGeluFp4) {
-          if (row < p.m) store_fp4<FMT>(p, to, v, row, col);
+          // the warp's 128 columns as one box of 64 bytes a row, and a row's scales as words
+          const bool last = j == 3 || col + 32 >= p.n;
+          uint32_t c[4], sb[2];
+          fp4_quant32<FMT>(v, to, c, sb);
+          if (j == 0) {
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+          }
+          // 64-byte swizzle: 16-byte unit j at j ^ (row / 2 % 4)
+          st_shared_v4(out0 + lane * 64 + 16 * (j ^ ((lane >> 1) & 3)), c[0], c[1], c[2], c[3]);
+          constexpr int PER = 32 / Fp4<FMT>::BLOCK;  // scales of 32 columns
+          scales |= (PER == 2 ? sb[0] | (sb[1] << 8) : sb[0]) << (8 * PER * (j % (4 / PER)));
+          if (j % (4 / PER) == 4 / PER - 1 || last) {
+            // a row that ends inside a group of four scales: the others are 0
+            if (row < p.m)
+              *reinterpret_cast<uint32_t *>(
+                  p.out_sf + mx_sf_offset(row, (col / Fp4<FMT>::BLOCK) & ~3,
+                                          (p.n / Fp4<FMT>::BLOCK + 3) / 4)) = scales;
+            scales = 0;
+          }
+          if (last) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tma_out, col0 / 2, row0, out0);
+              bulk_commit();
+            }
+          }
         } else if constexpr (EPI == kEpiGatedResidual) {
 #pragma unroll
           for (int q = 0; q < 8; ++q)

@@ -249,8 +249,7 @@ struct Fp4GemmPlan {
 Fp4GemmPlan fp4_gemm_plan(int fmt, Fp4GemmParams *p, int num_sms);
 // Codes as rows of bytes in boxes of 128 bytes; for a pair also the scale
 // arrays, as rows of 8-byte elements (a row: the scale blocks of 128 rows), and
-// the output in boxes of 32 rows x 128 bytes, 128-byte swizzle (unused where the
-// output is FP4).
+// the output in boxes of 32 rows x 128 bytes, 128-byte swizzle (FP4 rows: both 64).
 struct Fp4GemmMaps {
   CUtensorMap a, b, a_sf, b_sf, out;
 };
