@@ -529,20 +529,27 @@ cudaError_t launch(const Fp4GemmMaps &t, const Fp4GemmParams &p, const Fp4GemmPl
 // NVFP4 two k-blocks of columns; waiting for those cost more than the pause.
 //
 // The epilogue's rows go through shared memory (boxes of 32 rows x 128 bytes per
-// warp, 64 bytes with FP4 rows) and leave by TMA stores.
+// warp, 64 bytes with FP4 rows) and leave by TMA stores. With SHORT sums the
+// epilogue is what a tile waits for, and its warps wait for their loads and stores:
+// then it has 16 of them instead of 8, 64 columns each, and the ring one stage less.
+// NVFP4 8192 x 8192, 8 and 16 warps: GELU k 1024 89 and 73 us, 2048 94 and 87, 3584
+// 113 and 119; into the residual (5376 columns) 98 and 84, 101 and 91, 105 and 109;
+// stores 58 and 57, 75 and 83.
 namespace pair {
 constexpr int BN = 256;
-constexpr int PARTS = 2;         // epilogue warps per TMEM lane quarter
-constexpr int THREADS = 64 + 128 * PARTS;
-constexpr int STAGES = 5;
+// k-blocks up to which a sum is short.
+constexpr int short_blocks(int epi) { return epi == kEpiStore ? 4 : 8; }
 constexpr int A_BYTES = BM * BKB, B_BYTES = BN / 2 * BKB;
 constexpr int OUT_BYTES = 4096;  // per epilogue warp: a box of 32 rows x 128 bytes
 constexpr uint32_t SF_COL0 = BN;
 constexpr uint16_t kBothCtas = 0x3, kFirstCta = 0x1;
-static_assert(BN == 2 * 64 * PARTS, "two boxes of 64 columns per epilogue warp and tile");
 
-template <int FMT>
+template <int FMT, bool SHORT>
 struct Tile {
+  static constexpr int STAGES = SHORT ? 4 : 5;
+  static constexpr int PARTS = SHORT ? 4 : 2;  // epilogue warps per TMEM lane quarter
+  static constexpr int CHUNKS = BN / 32 / PARTS;  // 32 columns each, of one of them
+  static constexpr int THREADS = 64 + 128 * PARTS;
   static constexpr int SFA_BYTES = Kb<FMT>::CHUNKS * SF, SFB_BYTES = 2 * SFA_BYTES;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + SFA_BYTES + SFB_BYTES;
   static constexpr int NUM_BARS = 2 * STAGES + 3;
@@ -551,20 +558,27 @@ struct Tile {
   static constexpr int SMEM_BYTES = BARS_AT + 1024 + NUM_BARS * 8 + 16;
   static constexpr uint32_t SF_COLS = 12 * Kb<FMT>::CHUNKS;
 };
-static_assert(SF_COL0 + STAGES * Tile<kFp4Nv>::SF_COLS <= TMEM_COLS, "TMEM budget");
-static_assert(Tile<kFp4Nv>::STAGE_BYTES % 1024 == 0 && Tile<kFp4Mx>::STAGE_BYTES % 1024 == 0,
-              "stages start on swizzle atoms");
-static_assert(Tile<kFp4Nv>::SMEM_BYTES <= 227 * 1024, "shared memory budget");
+template <int FMT, bool SHORT>
+constexpr bool tile_ok() {
+  using T = Tile<FMT, SHORT>;
+  return SF_COL0 + T::STAGES * T::SF_COLS <= TMEM_COLS &&  // tensor memory
+         T::STAGE_BYTES % 1024 == 0 &&                     // stages start on swizzle atoms
+         T::SMEM_BYTES <= 227 * 1024;
+}
+static_assert(tile_ok<kFp4Nv, true>() && tile_ok<kFp4Nv, false>() && tile_ok<kFp4Mx, true>() &&
+                  tile_ok<kFp4Mx, false>(),
+              "tile sizes");
 
-template <int FMT, int EPI>
-__global__ void __launch_bounds__(THREADS, 1)
+template <int FMT, int EPI, bool SHORT>
+__global__ void __launch_bounds__(Tile<FMT, SHORT>::THREADS, 1)
     gemm_fp4_pair(const __grid_constant__ CUtensorMap tma_a,
                   const __grid_constant__ CUtensorMap tma_b,
                   const __grid_constant__ CUtensorMap tma_sfa,
                   const __grid_constant__ CUtensorMap tma_sfb,
                   const __grid_constant__ CUtensorMap tma_out, const Fp4GemmParams p) {
-  using T = Tile<FMT>;
+  using T = Tile<FMT, SHORT>;
   constexpr bool NV = FMT == kFp4Nv;
+  constexpr int STAGES = T::STAGES, PARTS = T::PARTS, CHUNKS = T::CHUNKS;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -732,7 +746,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
       const int row0 = (2 * tm + static_cast<int>(rank)) * BM + sub * 32;
       const int row = row0 + lane;
-      const int col0 = tn * BN + 128 * part;  // this warp's 128 columns, by 32
+      const int col0 = tn * BN + 32 * CHUNKS * part;  // this warp's columns, by 32
       uint32_t scales = 0;                    // of an FP4 output, being gathered
       // 32 columns of the warp's rows of the residual into its box, whole lines at
       // a time (a thread's own row at a time, the warps' lines did not fit into L1)
@@ -759,6 +773,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         float v[32];
         values<EPI>(p, al, r, col, [&](int q) { return ld_shared_v4(o + 16 * (q ^ (lane & 7))); }, v);
         if constexpr (EPI == kEpiGeluFp4) {
+          static_assert(CHUNKS == 4, "a box of 64 bytes a row");
           // the warp's 128 columns as one box of 64 bytes a row, and a row's scales as words
           const bool last = j == 3 || col + 32 >= p.n;
           uint32_t c[4], sb[2];
@@ -799,7 +814,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             tma_store_2d(&tma_out, col, row0, out0);
             bulk_commit();
           }
-          if (j < 3) fetch(j + 1);
+          if (j + 1 < CHUNKS) fetch(j + 1);
         } else {
           if ((j & 1) == 0) {
             if (lane == 0) bulk_wait_read<0>();
@@ -827,10 +842,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       const bool ok = mbar_wait(TFULL, full_phase, p.status);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
-      uint32_t r[4][32];
+      uint32_t r[CHUNKS][32];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) tmem_ld32_async(lanes + 128 * part + 32 * j, r[j]);
-      tmem_wait_ld(r[0], r[1], r[2], r[3]);
+      for (int j = 0; j < CHUNKS; ++j) tmem_ld32_async(lanes + 32 * (CHUNKS * part + j), r[j]);
+      tmem_wait_ld(r);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -840,7 +855,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           mbar_arrive_cluster(tempty);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) finish(j, r[j]);
+      for (int j = 0; j < CHUNKS; ++j) finish(j, r[j]);
       full_phase ^= 1;
     }
     cp_async_wait_all();
@@ -872,15 +887,16 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-template <int FMT, int EPI>
-cudaError_t launch(const Fp4GemmMaps &t, const Fp4GemmParams &p, int grid, cudaStream_t s) {
+template <int FMT, int EPI, bool SHORT>
+cudaError_t launch_tile(const Fp4GemmMaps &t, const Fp4GemmParams &p, int grid, cudaStream_t s) {
   static PerDevice smem_attr;
-  cudaError_t e = set_smem_once(smem_attr, gemm_fp4_pair<FMT, EPI>, Tile<FMT>::SMEM_BYTES);
+  using T = Tile<FMT, SHORT>;
+  cudaError_t e = set_smem_once(smem_attr, gemm_fp4_pair<FMT, EPI, SHORT>, T::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(THREADS, 1, 1);
-  cfg.dynamicSmemBytes = Tile<FMT>::SMEM_BYTES;
+  cfg.blockDim = dim3(T::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = T::SMEM_BYTES;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -889,7 +905,16 @@ cudaError_t launch(const Fp4GemmMaps &t, const Fp4GemmParams &p, int grid, cudaS
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, gemm_fp4_pair<FMT, EPI>, t.a, t.b, t.a_sf, t.b_sf, t.out, p);
+  return cudaLaunchKernelEx(&cfg, gemm_fp4_pair<FMT, EPI, SHORT>, t.a, t.b, t.a_sf, t.b_sf, t.out,
+                            p);
+}
+
+template <int FMT, int EPI>
+cudaError_t launch(const Fp4GemmMaps &t, const Fp4GemmParams &p, int grid, cudaStream_t s) {
+  // an FP4 row's box is as wide as 128 columns, so these stay with eight warps
+  if constexpr (EPI != kEpiGeluFp4)
+    if (p.k <= short_blocks(EPI) * BK) return launch_tile<FMT, EPI, true>(t, p, grid, s);
+  return launch_tile<FMT, EPI, false>(t, p, grid, s);
 }
 }  // namespace pair
 

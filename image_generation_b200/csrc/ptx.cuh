@@ -319,13 +319,11 @@ H3_DEV void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
                  "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
 H3_DEV void tmem_keep32(uint32_t (&r)[32]) { asm volatile("" : H3_K8(0), H3_K8(8), H3_K8(16), H3_K8(24)); }
 #undef H3_K8
-H3_DEV void tmem_wait_ld(uint32_t (&a)[32], uint32_t (&b)[32], uint32_t (&c)[32],
-                         uint32_t (&d)[32]) {
+template <int N>
+H3_DEV void tmem_wait_ld(uint32_t (&r)[N][32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-  tmem_keep32(a);
-  tmem_keep32(b);
-  tmem_keep32(c);
-  tmem_keep32(d);
+#pragma unroll
+  for (int i = 0; i < N; ++i) tmem_keep32(r[i]);
 }
 
 #define H3_W8(i) "r"(r[i + 0]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), \

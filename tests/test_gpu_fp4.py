@@ -210,7 +210,7 @@ def sum_bound(av, wv, k):
 @FMTS
 @pytest.mark.parametrize("gelu_tanh", [False, True], ids=["erf", "tanh"])
 @pytest.mark.parametrize("m,n,k", [(1, 64, 256), (5, 128, 704), (300, 320, 768), (385, 1024, 320), (6, 192, 6144),
-                                   (1301, 2112, 704)])
+                                   (1301, 2112, 704), (1301, 2112, 2368)])
 def test_linear_epilogues(ctx, fmt, gelu_tanh, m, n, k):
     from image_generation_b200 import h3dit as H
 
