@@ -91,34 +91,40 @@ H3_DEV void gelu2(float &a, float &b) {
 template <int EPI, int N, typename Resid>
 H3_DEV void values(const Fp4GemmParams &p, const Alpha &al, const uint32_t (&acc)[N], int col,
                    Resid &&resid, float (&v)[N]) {
+  // in packed pairs
+  uint64_t w[N / 2];
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = __uint_as_float(acc[i]) * al.a;
+  for (int i = 0; i < N / 2; ++i)
+    w[i] = f2_pack(__uint_as_float(acc[2 * i]), __uint_as_float(acc[2 * i + 1]));
   if (al.b != 1.f) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) v[i] *= al.b;
+    for (int i = 0; i < N / 2; ++i) w[i] = f2_mul(w[i], f2_pack(al.b, al.b));
   }
+  const uint64_t alpha = f2_pack(al.a, al.a);
   if (p.bias) {
     const float4 *b = reinterpret_cast<const float4 *>(p.bias + col);
 #pragma unroll
     for (int q = 0; q < N / 4; ++q) {
       const float4 bb = __ldg(b + q);
-      v[4 * q + 0] += bb.x;
-      v[4 * q + 1] += bb.y;
-      v[4 * q + 2] += bb.z;
-      v[4 * q + 3] += bb.w;
+      w[2 * q] = f2_fma(w[2 * q], alpha, f2_pack(bb.x, bb.y));
+      w[2 * q + 1] = f2_fma(w[2 * q + 1], alpha, f2_pack(bb.z, bb.w));
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) w[i] = f2_mul(w[i], alpha);
   }
   if constexpr (EPI == kEpiGatedResidual) {
     const float4 *g = reinterpret_cast<const float4 *>(p.gate + col);
 #pragma unroll
     for (int q = 0; q < N / 4; ++q) {
       const float4 gg = __ldg(g + q), x = resid(q);
-      v[4 * q + 0] = fmaf(gg.x, v[4 * q + 0], x.x);
-      v[4 * q + 1] = fmaf(gg.y, v[4 * q + 1], x.y);
-      v[4 * q + 2] = fmaf(gg.z, v[4 * q + 2], x.z);
-      v[4 * q + 3] = fmaf(gg.w, v[4 * q + 3], x.w);
+      w[2 * q] = f2_fma(f2_pack(gg.x, gg.y), w[2 * q], f2_pack(x.x, x.y));
+      w[2 * q + 1] = f2_fma(f2_pack(gg.z, gg.w), w[2 * q + 1], f2_pack(x.z, x.w));
     }
-  } else if constexpr (EPI != kEpiStore) {
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) f2_unpack(w[i], v[2 * i], v[2 * i + 1]);
+  if constexpr (EPI == kEpiGelu || EPI == kEpiGeluFp4) {
     // one branch for all, not one each
     if (p.gelu_tanh) {
 #pragma unroll
