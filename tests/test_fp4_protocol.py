@@ -121,9 +121,10 @@ def simulate_split(kblocks, rng, stages):
 
 
 @pytest.mark.parametrize("tiles,kblocks", [(1, 1), (2, 1), (7, 1), (1, 9), (3, 4), (4, 5), (5, 6), (3, 21)])
-def test_pair_runs_to_the_end(tiles, kblocks):
-    for seed in range(40):
-        assert simulate_pair(tiles, kblocks, random.Random(seed))
+@pytest.mark.parametrize("stages,warps", [(5, 8), (4, 16)], ids=["long", "short"])
+def test_pair_runs_to_the_end(tiles, kblocks, stages, warps):
+    for seed in range(30):
+        assert simulate_pair(tiles, kblocks, random.Random(seed), stages, warps)
 
 
 @pytest.mark.parametrize("kblocks", [1, 2, 3, 4, 5, 9, 16])
