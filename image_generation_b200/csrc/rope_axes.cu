@@ -269,20 +269,29 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
       }
       if (live) {
         Eight x, y;
+        if (PARTIAL && 8 * u >= turning) {
+          // passes through, and stays out of its neighbour, an infinity too
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x.v[i] = f2_fma(a.v[i], ac.v[i], f2_mul(b.v[i], bs.v[i]));
-          y.v[i] = f2_fma(b.v[i], bc.v[i], f2_mul(a.v[i], as.v[i]));
+          for (int i = 0; i < 4; ++i) {
+            x.v[i] = f2_mul(a.v[i], ac.v[i]);
+            y.v[i] = f2_mul(b.v[i], bc.v[i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x.v[i] = f2_fma(a.v[i], ac.v[i], f2_mul(b.v[i], bs.v[i]));
+            y.v[i] = f2_fma(b.v[i], bc.v[i], f2_mul(a.v[i], as.v[i]));
+          }
         }
-        if (PARTIAL && turning < 8 * u + 8) {
-          // what passes through stays out of its neighbour, an infinity too: from the
-          // ring again, so that the others keep no registers for this
+        if (PARTIAL && turning % 8 && u == turning / 8) {
+          // the lane in which the rotation ends: its other pairs from the ring again, so
+          // that the rest keeps no registers for this
           float fx[8], fy[8];
           floats(x, fx);
           floats(y, fy);
           const float *weight = w ? p.weight[1] : p.weight[0];
 #pragma unroll 1
-          for (int i = max(0, turning - 8 * u); i < 8; ++i) {
+          for (int i = turning % 8; i < 8; ++i) {
             Pair q{16 * u + 2 * i, 16 * u + 2 * i + 1};
             if (ORDER != kInterleaved) q = split_pair(p, 8 * u + i);
             const T *type = nullptr;
