@@ -18,7 +18,7 @@
 // fp64 (far positions). The warp's next heads are on their way to shared memory
 // (cp.async, whole lines at a time).
 // 16896 tokens x 112 heads x 96: 118 us, 6.1 TB/s (181 with cosines in shared
-// memory per head, 164 with loads to registers); 20736 x 64 x 128, neighbours: 112.
+// memory per head, 164 with loads to registers); 20736 x 64 x 128, neighbours: 111.
 #include <type_traits>
 
 #include "kernels.h"
@@ -153,6 +153,41 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
   if (task >= tasks) return;
   const long long t = task / parts;
   const int part = static_cast<int>(task - t * parts);
+  // this part's rounds of GROUPS heads: q's, then k's
+  auto rounds_of = [&](int heads) { return (heads + GROUPS - 1) / GROUPS; };
+  auto first_of = [&](int heads, int i) { return rounds_of(heads) * i / parts; };
+  // on their way to shared memory one after another, whole lines at a time
+  uint32_t to = ring;
+  int which = 0, ahead = 0, left = 0;  // of the matrix being fetched: rounds, 16-byte pieces
+  const uint8_t *from = nullptr;
+  auto begin = [&](int w) {
+    const int heads = w ? p.heads[1] : p.heads[0];
+    const int r0 = first_of(heads, part), r1 = first_of(heads, part + 1);
+    const T *src = w ? static_cast<const T *>(p.src[1]) + t * p.ld_src[1]
+                     : static_cast<const T *>(p.src[0]) + t * p.ld_src[0];
+    which = w;
+    ahead = r1 - r0;
+    from = reinterpret_cast<const uint8_t *>(src + r0 * stride) + 16 * lane;
+    left = (min(r1 * GROUPS, heads) - r0 * GROUPS) * p.head_dim * static_cast<int>(sizeof(T)) / 16 -
+           lane;
+  };
+  auto fetch = [&] {
+    if (ahead == 0 && which == 0) begin(1);
+    if (ahead > 0) {
+#pragma unroll
+      for (int i = 0; i < static_cast<int>(ROUND / 512); ++i)
+        if (32 * i + lane < round_units && 32 * i < left)
+          cp_async16(to + 16 * lane + 512 * i, from + 512 * i);
+      from += stride * sizeof(T);
+      left -= round_units;
+      --ahead;
+    }
+    cp_async_commit();
+    to = to == ring + (kDepth - 1) * ROUND ? ring : to + ROUND;
+  };
+  begin(0);
+#pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) fetch();
   for (int pair = lane; pair < half; pair += 32) {
     float c = 1.f, s = 0.f;  // where nothing turns
     if (pair < turning) {
@@ -167,38 +202,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     cs[warp][1][pair] = s;
   }
   __syncwarp();
+  uint32_t at = ring;
 #pragma unroll 1
   for (int w = 0; w < 2; ++w) {
-    // this part's share of the heads, in rounds of GROUPS
     const int heads = w ? p.heads[1] : p.heads[0];
-    const int rounds = (heads + GROUPS - 1) / GROUPS;
-    const int r0 = rounds * part / parts, r1 = rounds * (part + 1) / parts;
+    const int r0 = first_of(heads, part), r1 = first_of(heads, part + 1);
     if (r0 >= r1) continue;
     int head = r0 * GROUPS + group;  // of this lane in the round at hand
-    const int last = min(r1 * GROUPS, heads);
-    const int end = on ? last : 0;
-    const T *src = w ? static_cast<const T *>(p.src[1]) + t * p.ld_src[1]
-                     : static_cast<const T *>(p.src[0]) + t * p.ld_src[0];
+    const int end = on ? min(r1 * GROUPS, heads) : 0;
     T *dst = w ? static_cast<T *>(p.dst[1]) + t * p.ld_dst[1]
                : static_cast<T *>(p.dst[0]) + t * p.ld_dst[0];
     dst += head * p.head_dim;
-    // rounds on their way to shared memory, whole lines at a time
-    const uint8_t *from = reinterpret_cast<const uint8_t *>(src + r0 * stride) + 16 * lane;
-    int left = (last - r0 * GROUPS) * p.head_dim * static_cast<int>(sizeof(T)) / 16 - lane;
-    uint32_t to = ring;
-    auto fetch = [&] {
-#pragma unroll
-      for (int i = 0; i < static_cast<int>(ROUND / 512); ++i)
-        if (32 * i + lane < round_units && 32 * i < left)
-          cp_async16(to + 16 * lane + 512 * i, from + 512 * i);
-      cp_async_commit();
-      from += stride * sizeof(T);
-      left -= round_units;
-      to = to == ring + (kDepth - 1) * ROUND ? ring : to + ROUND;
-    };
-    __syncwarp();  // the ring has been read
-#pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) fetch();
     // x = a (wa c) - b (wb s), y = b (wb c) + a (wa s)
     Eight ac = shared8(&cs[warp][0][on ? 8 * u : 0]), as = shared8(&cs[warp][1][on ? 8 * u : 0]);
     Eight bc = ac, bs = as;
@@ -223,7 +237,6 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) bs.v[i] = f2_mul(bs.v[i], f2_pack(-1.f, -1.f));
-    uint32_t at = ring;
 #pragma unroll 1
     for (int r = r0; r < r1; ++r) {
       __syncwarp();  // the round before has been read: its place is free
@@ -283,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm)
             y.v[i] = f2_fma(b.v[i], bc.v[i], f2_mul(a.v[i], as.v[i]));
           }
         }
-        if (PARTIAL && turning % 8 && u == turning / 8) {
+        if (PARTIAL && ORDER != kSplit8 && turning % 8 && u == turning / 8) {
           // the lane in which the rotation ends: its other pairs from the ring again, so
           // that the rest keeps no registers for this
           float fx[8], fy[8];
