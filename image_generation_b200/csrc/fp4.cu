@@ -163,8 +163,9 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Largest finite magnitude of the matrix over 2688 = 6 * 448 (1 for a matrix
-// of zeros). Each block leaves its maximum in `part`; the block that finds
+// Largest finite magnitude of the matrix over 2688 = 6 * 448, at least 2^-149 (1
+// for a matrix of zeros): a scale of 0 would make NaN of a matrix whose quotient
+// rounds to 0, where 2^-149 gives zeros, as the scales just above it do. Each block leaves its maximum in `part`; the block that finds
 // itself last (by `done`, which it sets back to 0) joins them. A maximum does
 // not depend on the order, so neither does the result.
 template <typename T>
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();  // red[] is read above by every thread
   m = block_max(m);
   if (threadIdx.x == 0) {
-    *out = m > 0.f ? __fdiv_rn(m, 2688.f) : 1.f;
+    *out = m > 0.f ? fmaxf(__fdiv_rn(m, 2688.f), __uint_as_float(1u)) : 1.f;
     *done = 0;
   }
 }

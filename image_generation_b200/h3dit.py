@@ -639,8 +639,8 @@ class Context:
         return ptr, src.dtype == torch.float32, ld, rows, k
 
     def fp4_tensor_scale(self, src, scale_out, stream=None) -> None:
-        """scale_out (one fp32) = src's largest finite magnitude over 2688 (1 if
-        that is 0): what an NVFP4 matrix of src is quantized under."""
+        """scale_out (one fp32) = src's largest finite magnitude over 2688, at
+        least 2^-149 (1 for a matrix of zeros): what an NVFP4 matrix of src is quantized under."""
         if scale_out is None:
             raise _bad("scale_out is needed")
         self._check(lib.h3dit_fp4_tensor_scale(self.handle, *self._fp4_source(src),

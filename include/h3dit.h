@@ -445,10 +445,11 @@ h3dit_status h3dit_attention_mx(h3dit_ctx *ctx, const void *q, const void *k, co
 size_t h3dit_fp4_scale_bytes(int32_t format, int32_t rows, int32_t k);
 
 /* *scale_out (device fp32) = largest finite magnitude of src over 2688 = 6 * 448,
- * or 1 for a matrix of zeros: the tensor scale of src in NVFP4. src: device bf16
- * [rows, k], fp32 if src_fp32 is 1, k a multiple of 64, row stride ld elements (a
- * multiple of 16 bytes). rows 0 leaves *scale_out as it is. Uses the context's
- * workspace. */
+ * at least 2^-149, or 1 for a matrix of zeros: the tensor scale of src in NVFP4.
+ * (Under scales below about 2^-135 every element is 0: d < 2^-126 in all blocks.)
+ * src: device bf16 [rows, k], fp32 if src_fp32 is 1, k a multiple of 64, row
+ * stride ld elements (a multiple of 16 bytes). rows 0 leaves *scale_out as it is.
+ * Uses the context's workspace. */
 h3dit_status h3dit_fp4_tensor_scale(h3dit_ctx *ctx, const void *src, int32_t src_fp32, int64_t ld,
                                     int32_t rows, int32_t k, float *scale_out, void *cuda_stream);
 

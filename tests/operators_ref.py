@@ -46,7 +46,7 @@ def tensor_scale(x):
     a = np.abs(np.asarray(x, F32))
     a = a[np.isfinite(a)]
     m = a.max() if a.size else F32(0)
-    return F32(m / F32(2688)) if m > 0 else F32(1)
+    return max(F32(m / F32(2688)), F32(2.0 ** -149)) if m > 0 else F32(1)
 
 
 def quantize(fmt, x, g=None):

@@ -147,6 +147,36 @@ def test_tensor_scale_skips_non_finite_and_repeats(ctx):
     ok(ctx)
 
 
+@pytest.mark.parametrize("f32", [True, False], ids=["f32", "bf16"])
+@pytest.mark.parametrize("size", [2.0 ** -149, 2.0 ** -140, 1.8e-42, 2e-42, 1e-40, 1e-38])
+def test_tiny_matrices_stay_finite(ctx, size, f32):
+    """Magnitudes down to the smallest: the tensor scale is never 0, and what the
+    matrix stands for, alone and in a product, is finite (zeros at the lowest)."""
+    from image_generation_b200 import h3dit as H
+
+    x = np.zeros((3, 128), np.float32)
+    x[0, 5], x[1, 64:] = size, -size
+    x = x if f32 else bf16(x).astype(np.float32)
+    g = R.tensor_scale(x)
+    assert g > 0
+    t = torch.full((1,), -1.0, device="cuda")
+    ctx.fp4_tensor_scale(src_tensor(x, f32), t)
+    assert t.item() == float(g)
+    q = torch.zeros(3, 64, dtype=torch.uint8, device="cuda")
+    sf = torch.zeros(R.sf_bytes(R.NV, 3, 128), dtype=torch.uint8, device="cuda")
+    out, prod = (torch.full((3, n), float("nan"), dtype=torch.bfloat16, device="cuda") for n in (128, 32))
+    ctx.fp4_quantize(R.NV, src_tensor(x, f32), q, sf, tensor_scale=t)
+    ctx.fp4_dequantize(R.NV, q, sf, out, tensor_scale=t)
+    w, wsf, _ = operand(R.NV, 32, 128, 1, True)
+    ctx.linear_fp4(R.NV, H.H3DIT_EPI_STORE, q, sf, w, wsf, prod, a_scale=t)
+    ok(ctx)
+    codes, byte = R.quantize(R.NV, x, g)
+    ref = R.values(R.NV, codes, byte, g)
+    # two fp32 products, one of them perhaps subnormal (2^-150), and one bf16 rounding (2^-134)
+    assert np.all(np.abs(to_np(out) - ref) <= (2.0 ** -8 + 2.0 ** -23) * np.abs(ref) + 2.0 ** -133)
+    assert torch.isfinite(prod).all()
+
+
 # ------------------------------------------------------------------------ product
 
 def operand(fmt, rows, k, seed, exact, g=None):
