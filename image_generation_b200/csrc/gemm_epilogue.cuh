@@ -51,7 +51,9 @@ __device__ __forceinline__ float erf_nonneg(float z) {
 __device__ __forceinline__ float gelu_f(float x, int tanh_form) {
   if (tanh_form) {
     const float u = 0.7978845608028654f * (x + 0.044715f * x * x * x);
-    return 0.5f * x * (1.0f + tanhf(u));
+    // finite where tanh is -1: minus infinity gives 0, not infinity * 0 (a NaN stays one)
+    const float xf = x < -3e38f ? -3e38f : x;
+    return 0.5f * xf * (1.0f + tanhf(u));
   }
   // x Phi(x) = x (1 + erf(x / sqrt 2)) / 2, erf odd
   const float er = copysignf(erf_nonneg(fabsf(x) * 0.7071067811865476f), x);

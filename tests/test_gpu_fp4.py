@@ -375,6 +375,42 @@ def test_sums_past_fp32_and_their_gelu(ctx, m):
         assert np.all(got[1] == want[0]) and np.all(got[2] == want[1])
 
 
+@FMTS
+@pytest.mark.parametrize("gelu_tanh", [False, True], ids=["erf", "tanh"])
+@pytest.mark.parametrize("m", [3, 1300], ids=["few_rows", "pairs"])
+def test_gelu_of_sums_past_fp32(ctx, fmt, gelu_tanh, m):
+    """GELU in either form, to bf16 and to FP4: of minus infinity 0, of plus infinity
+    itself (to FP4 a NaN block), of a NaN a NaN, other rows as ever."""
+    from image_generation_b200 import h3dit as H
+
+    c = make_ctx(gelu_tanh=True) if gelu_tanh else ctx
+    n, k = 2112, 128
+    codes = np.full((m, k), 2, np.uint8)                  # ones, then minus ones
+    codes[2] = 10
+    unit = 127 if fmt == R.MX else 0x38
+    byte = np.full((m, k // R.BLOCK[fmt]), unit, np.uint8)
+    byte[0] = 255 if fmt == R.MX else 127
+    wb = np.full((n, k // R.BLOCK[fmt]), unit, np.uint8)
+    bias = np.zeros(n, np.float32)
+    w, wsf = dev(R.pack(np.full((n, k), 2, np.uint8))), dev(R.sf_layout(wb))
+    # a_scale: sums of 128 past fp32 in rows 1 and 2; the others are 0 times that
+    codes[3:] = 0
+    kw = dict(a_scale=dev(np.array([3e38], np.float32)), bias=dev(bias))
+    a, asf = dev(R.pack(codes)), dev(R.sf_layout(byte))
+    out = torch.full((m, n), 9.0, dtype=torch.bfloat16, device="cuda")
+    c.linear_fp4(fmt, H.H3DIT_EPI_GELU, a, asf, w, wsf, out, **kw)
+    q = torch.zeros(m, n // 2, dtype=torch.uint8, device="cuda")
+    sf = torch.zeros(R.sf_bytes(fmt, m, n), dtype=torch.uint8, device="cuda")
+    c.linear_fp4(fmt, H.H3DIT_EPI_GELU, a, asf, w, wsf, q, out_sf=sf, **kw)
+    vals = torch.full((m, n), 9.0, dtype=torch.bfloat16, device="cuda")
+    c.fp4_dequantize(fmt, q, sf, vals)
+    ok(c)
+    for got, inf in ((to_np(out), np.inf), (to_np(vals), np.nan)):
+        assert np.isnan(got[0]).all()
+        assert np.array_equal(got[1], np.full(n, inf), equal_nan=True)
+        assert not got[2:].any()
+
+
 def test_offsets_past_31_bits(ctx):
     """More than 2^31 elements in and out: the last rows as when they come alone."""
     from image_generation_b200 import h3dit as H
