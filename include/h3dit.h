@@ -515,8 +515,11 @@ typedef struct h3dit_norm_args {
 /* The norms on either side of a residual addition, in one pass per row:
  *   x' = r x + gate * (post_norm ? RMSNorm(branch) post_weight : branch)
  *   out = RMSNorm(x') pre_weight (1 + scale) + shift
- * with RMSNorm(v) = v / sqrt(mean(v^2) + norm_eps); x' in fp32, out rounded once
- * to its kind. D is the context's hidden. A row with a NaN is NaN in both. */
+ * with RMSNorm(v) = v / sqrt(mean(v^2) + norm_eps), its sums of squares in fp32;
+ * x' in fp32, out rounded once to its kind. D is the context's hidden. A NaN in
+ * a row of x, or of the branch without post_norm, makes that element of x' NaN;
+ * in the branch with post_norm the whole row of x'. The row of out is NaN in
+ * every element (every scale, with FP4 rows) wherever its row of x' has one. */
 h3dit_status h3dit_gated_norm(h3dit_ctx *ctx, const h3dit_norm_args *args, void *cuda_stream);
 
 /* Rotary positions on three axes: the head's first 2 (s0 + s1 + s2) elements

@@ -179,6 +179,36 @@ def test_zero_rows_and_nan_rows(ctxs):
     assert np.all(b[3] == 0x7f) and not np.any(b[keep] == 0x7f)
 
 
+@pytest.mark.parametrize("kind", [0, 1, 2, 3], ids=["bf16", "mxfp8", "mxfp4", "nvfp4"])
+@pytest.mark.parametrize("post", [False, True], ids=["plain", "post"])
+@pytest.mark.parametrize("where", ["x", "branch"])
+def test_where_a_nan_goes(ctxs, where, post, kind):
+    """x' is NaN where x or the branch is, all along the row if a normed branch has
+    one; out all along the row in any case; other rows know nothing of it."""
+    n, d, row, col = 5, 768, 2, 333
+    ctx = ctx_for(ctxs, d)
+    i = inputs(n, d, 1, 21, True)
+    clean = run(ctx, i, n, d, 1, post, True, kind, ALL, t=np.float32(0.02) if kind == 3 else None)
+    i["x" if where == "x" else "y"][row, col] = np.nan
+    xo, out, sf, *_ = run(ctx, i, n, d, 1, post, True, kind, ALL, t=np.float32(0.02) if kind == 3 else None)
+    nan = torch.isnan(xo)
+    want = torch.zeros_like(nan)
+    want[row, slice(None) if where == "branch" and post else col] = True
+    assert torch.equal(nan, want)
+    keep = [r for r in range(n) if r != row]
+    assert torch.equal(xo[keep], clean[0][keep])
+    if kind == 0:
+        assert torch.isnan(out[row]).all() and torch.equal(out[keep], clean[1][keep])
+    elif kind == 1:
+        assert (out.view(n, d)[row] & 127 == 127).all()   # E4M3 NaN
+        assert torch.equal(out.view(n, d)[keep], clean[1].view(n, d)[keep])
+    else:
+        at = R.sf_index(n, d // (32 if kind == 2 else 16))
+        got, ref = (s.cpu().numpy()[at] for s in (sf, clean[2]))
+        assert np.all(got[row] == (255 if kind == 2 else 127))
+        assert np.array_equal(got[keep], ref[keep]) and torch.equal(out[keep], clean[1][keep])
+
+
 def test_more_rows_than_ctas_match_alone(ctxs):
     """A row's result does not depend on the rows beside it or on the launch."""
     n, d = 6000, 768
