@@ -34,7 +34,7 @@ constexpr size_t kNoTiled = ~static_cast<size_t>(0);
 
 struct Layout {
   size_t status, resid, xm, qkv, attn, u, mod, cvec, hidden, omod, rope, wptr, bptr;
-  size_t amax;  // fp4_tensor_scale: its counter (kAlign bytes), then the partial maxima
+  size_t amax;  // fp4_tensor_scale: the partial maxima
   // MXFP8 precision only
   size_t xq, xq_sf, oq, oq_sf, uq, uq_sf, wq, wq_block;
   MxWeights wq_off;  // offsets inside one block's slice of the wq arena
@@ -83,7 +83,7 @@ Layout plan(const h3dit_config *c) {
   L.rope = take(N * (c->head_dim / 2) * 2 * 4);
   L.wptr = take(static_cast<size_t>(c->n_blocks) * sizeof(void *));
   L.bptr = take(static_cast<size_t>(c->n_blocks) * sizeof(void *));
-  L.amax = take(kAlign + kFp4ScaleParts * sizeof(float));
+  L.amax = take(kFp4ScaleParts * sizeof(float));
   if (c->precision == H3DIT_PRECISION_MXFP8) {
     L.xq = take(N * D);
     L.xq_sf = take(mx_sf_bytes(N, D));
@@ -238,8 +238,7 @@ struct h3dit_ctx {
   std::vector<h3dit_vae_layer_weights> vlayers;
   size_t vpos = 0, vones = 0;  // workspace offsets: position table, a vector of ones
 
-  unsigned *amax_done() { return reinterpret_cast<unsigned *>(ws + L.amax); }
-  float *amax_part() { return reinterpret_cast<float *>(ws + L.amax + kAlign); }
+  float *amax_part() { return reinterpret_cast<float *>(ws + L.amax); }
   int *status() { return reinterpret_cast<int *>(ws + L.status); }
   float *resid() { return reinterpret_cast<float *>(ws + L.resid); }
   void *xm() { return ws + L.xm; }
@@ -967,7 +966,6 @@ h3dit_status h3dit_create(const h3dit_config *cfg, const h3dit_time_weights *tim
     bp[l] = blocks[l].b_ada;
   }
   cudaError_t e = cudaMemsetAsync(ctx->status(), 0, sizeof(int), s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(ctx->amax_done(), 0, sizeof(unsigned), s);
   if (e == cudaSuccess)
     e = cudaMemcpyAsync(ctx->ws + L.wptr, wp.data(), wp.size() * sizeof(void *),
                         cudaMemcpyHostToDevice, s);
@@ -1547,7 +1545,6 @@ h3dit_status h3dit_vae_create(const h3dit_vae_config *cfg, const h3dit_vae_weigh
   ctx->device = dev;
   std::vector<float> ones(cfg->width, 1.0f);
   cudaError_t e = cudaMemsetAsync(ctx->status(), 0, sizeof(int), s);
-  if (e == cudaSuccess) e = cudaMemsetAsync(ctx->amax_done(), 0, sizeof(unsigned), s);
   if (e == cudaSuccess)
     e = launch_vae_pos_table(cfg->tile, cfg->width, reinterpret_cast<float *>(ctx->ws + ctx->vpos),
                              ctx->num_sms, s);
@@ -1816,9 +1813,9 @@ h3dit_status h3dit_fp4_tensor_scale(h3dit_ctx *ctx, const void *src, int32_t src
     return ctx->fail(H3DIT_ERR_INVALID_ARG, "scale_out is NULL or misaligned");
   if ((st = check_device(ctx))) return st;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  Launch L(ctx, H3DIT_KERNEL_FP4_QUANTIZE, s);
+  Launch L(ctx, H3DIT_KERNEL_FP4_QUANTIZE, s, 2);
   return ctx->cuda(launch_fp4_tensor_scale(src, src_fp32 != 0, ld, rows, k, ctx->amax_part(),
-                                           ctx->amax_done(), scale_out, ctx->num_sms, s),
+                                           scale_out, ctx->num_sms, s),
                    "FP4 tensor scale launch");
 }
 

@@ -10,7 +10,7 @@
 // bytes into one store. The quantization goes from the matrix's end to its
 // beginning: what the tensor scale's pass read last is still in L2, and what it
 // writes last is what a reader from the beginning wants first. 16896 x 5376 of
-// bf16, NVFP4: tensor scale 30 us (6.0 TB/s), quantization 42 (5.5), values 38
+// bf16, NVFP4: tensor scale 29 us (6.2 TB/s), quantization 42 (5.5), values 38
 // (6.1); one after another 118.
 #include "fp4.cuh"
 
@@ -165,16 +165,29 @@ __global__ void __launch_bounds__(kThreads)
 
 // Largest finite magnitude of the matrix over 2688 = 6 * 448, at least 2^-149 (1
 // for a matrix of zeros): a scale of 0 would make NaN of a matrix whose quotient
-// rounds to 0, where 2^-149 gives zeros, as the scales just above it do. Each block leaves its maximum in `part`; the block that finds
-// itself last (by `done`, which it sets back to 0) joins them. A maximum does
-// not depend on the order, so neither does the result.
+// rounds to 0, where 2^-149 gives zeros, as the scales just above it do. Each block
+// leaves its maximum in `part`, and a block of a second launch joins them: a maximum
+// does not depend on the order, so neither does the result, and nothing that an
+// earlier call left in `part` is read. (A counter by which the last block of one launch
+// joins them makes every later scale wrong once it is off 0, by a call cut short or,
+// against the rule, overlapped by another of its context. 16896 x 5376 of bf16: 29.1 us;
+// with such a counter 30.2, and 33.9 where it is set to 0 before each launch.)
+H3_DEV float block_max(float x, float *red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+  __syncthreads();
+  float r = red[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 32; ++w) r = fmaxf(r, red[w]);
+  return r;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-    fp4_tensor_scale_kernel(const T *__restrict__ src, long long ld, bool wide, long long rows, int k,
-                            float *__restrict__ part, unsigned *__restrict__ done,
-                            float *__restrict__ out) {
+    fp4_amax_kernel(const T *__restrict__ src, long long ld, bool wide, long long rows, int k,
+                    float *__restrict__ part) {
   __shared__ float red[kThreads / 32];
-  __shared__ bool last;
   const int per_row = k / 16;
   const long long step = static_cast<long long>(gridDim.x) * kThreads;
   float m = 0.f;
@@ -190,34 +203,20 @@ __global__ void __launch_bounds__(kThreads)
       m = a < INFINITY ? fmaxf(m, a) : m;
     }
   }
-  auto block_max = [&](float x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-    __syncthreads();
-    float r = red[0];
-#pragma unroll
-    for (int w = 1; w < kThreads / 32; ++w) r = fmaxf(r, red[w]);
-    return r;
-  };
-  m = block_max(m);
-  if (threadIdx.x == 0) {
-    part[blockIdx.x] = m;
-    __threadfence();
-    last = atomicAdd(done, 1u) == gridDim.x - 1;
-  }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
-  m = 0.f;
-  for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += kThreads)
-    m = fmaxf(m, __ldcg(part + i));
-  __syncthreads();  // red[] is read above by every thread
-  m = block_max(m);
-  if (threadIdx.x == 0) {
+  m = block_max(m, red);
+  if (threadIdx.x == 0) part[blockIdx.x] = m;
+}
+
+// Launched while the kernel above still runs: its block is in place when that ends.
+__global__ void __launch_bounds__(kThreads)
+    fp4_tensor_scale_kernel(const float *__restrict__ part, int parts, float *__restrict__ out) {
+  __shared__ float red[kThreads / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // until the parts are written
+  float m = 0.f;
+  for (int i = threadIdx.x; i < parts; i += kThreads) m = fmaxf(m, __ldcg(part + i));
+  m = block_max(m, red);
+  if (threadIdx.x == 0)
     *out = m > 0.f ? fmaxf(__fdiv_rn(m, 2688.f), __uint_as_float(1u)) : 1.f;
-    *done = 0;
-  }
 }
 
 int grid_for(long long units, int num_sms, int per_sm) {
@@ -261,19 +260,28 @@ cudaError_t launch_fp4_dequantize(int fmt, const uint8_t *q, const uint8_t *sf, 
 }
 
 cudaError_t launch_fp4_tensor_scale(const void *src, bool f32, long long ld, int rows, int k,
-                                    float *part, unsigned *done, float *out, int num_sms,
-                                    cudaStream_t s) {
+                                    float *part, float *out, int num_sms, cudaStream_t s) {
   const long long units = static_cast<long long>(rows) * (k / 16);
   int grid = grid_for(units, num_sms, 8);
   if (grid > kFp4ScaleParts) grid = kFp4ScaleParts;
   const bool wide = is_wide(src, ld * (f32 ? 4 : 2));
   if (f32)
-    fp4_tensor_scale_kernel<<<grid, kThreads, 0, s>>>(static_cast<const float *>(src), ld, wide, rows,
-                                                      k, part, done, out);
+    fp4_amax_kernel<<<grid, kThreads, 0, s>>>(static_cast<const float *>(src), ld, wide, rows, k, part);
   else
-    fp4_tensor_scale_kernel<<<grid, kThreads, 0, s>>>(static_cast<const uint16_t *>(src), ld, wide,
-                                                      rows, k, part, done, out);
-  return cudaGetLastError();
+    fp4_amax_kernel<<<grid, kThreads, 0, s>>>(static_cast<const uint16_t *>(src), ld, wide, rows, k,
+                                              part);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(1, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fp4_tensor_scale_kernel, static_cast<const float *>(part), grid, out);
 }
 
 }  // namespace h3

@@ -219,10 +219,9 @@ cudaError_t launch_fp4_quantize(int fmt, const void *src, bool f32, long long ld
                                 cudaStream_t s);
 cudaError_t launch_fp4_dequantize(int fmt, const uint8_t *q, const uint8_t *sf, int rows, int k,
                                   const float *g, void *out, int num_sms, cudaStream_t s);
-// part: kFp4ScaleParts floats of scratch; done: a counter that is 0 between calls.
+// part: kFp4ScaleParts floats of scratch; what they hold before is of no account. Two kernels.
 cudaError_t launch_fp4_tensor_scale(const void *src, bool f32, long long ld, int rows, int k,
-                                    float *part, unsigned *done, float *out, int num_sms,
-                                    cudaStream_t s);
+                                    float *part, float *out, int num_sms, cudaStream_t s);
 
 // The product of two FP4 matrices (gemm_fp4.cu).
 struct Fp4GemmParams {

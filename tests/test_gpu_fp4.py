@@ -177,6 +177,31 @@ def test_tiny_matrices_stay_finite(ctx, size, f32):
     assert torch.isfinite(prod).all()
 
 
+def test_tensor_scale_needs_nothing_of_its_scratch():
+    """Whatever an earlier call, or an overlap that the rules forbid, left in the
+    workspace: the scale is right, eagerly and replayed."""
+    c = make_ctx()
+    x = source(3000, 768, 1, False)
+    xt, t = src_tensor(x, False), torch.full((1,), -1.0, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    c.fp4_tensor_scale(xt, t)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        c.fp4_tensor_scale(xt, t)
+    for byte in (0, 1, 0x5A, 0xFF):
+        for go in (lambda: c.fp4_tensor_scale(xt, t), graph.replay):
+            c.workspace[256:].fill_(byte)   # all but the status word
+            t.fill_(-1.0)
+            go()
+            ok(c)
+            assert t.item() == float(R.tensor_scale(x)), byte
+    # fewer blocks after more, and more after fewer
+    for rows in (1, 3000, 5, 700):
+        c.fp4_tensor_scale(xt[:rows], t)
+        assert t.item() == float(R.tensor_scale(x[:rows]))
+    ok(c)
+
+
 # ------------------------------------------------------------------------ product
 
 def operand(fmt, rows, k, seed, exact, g=None):
