@@ -108,16 +108,13 @@ H3_DEV void fp4_quant32(const float (&v)[32], const Fp4Tensor &t, uint32_t (&q)[
   }
 }
 
-// What a scale byte stands for, with the tensor scale.
+// What a scale byte stands for.
 template <int FMT>
-H3_DEV float fp4_scale_value(uint32_t sb, float g) {
-  if constexpr (FMT == kFp4Mx) {
-    const float s = sb == 0 ? __uint_as_float(0x00400000u)
-                            : __uint_as_float(sb == 255u ? 0x7fc00000u : sb << 23);
-    return __fmul_rn(s, g);
-  } else {
-    return __fmul_rn(e4m3_to_float(sb), g);
-  }
+H3_DEV float fp4_scale_value(uint32_t sb) {
+  if constexpr (FMT == kFp4Mx)
+    return sb == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(sb == 255u ? 0x7fc00000u : sb << 23);
+  else
+    return e4m3_to_float(sb);
 }
 
 }  // namespace h3

@@ -459,8 +459,9 @@ h3dit_status h3dit_fp4_quantize(h3dit_ctx *ctx, int32_t format, const void *src,
                                 int64_t ld, int32_t rows, int32_t k, const float *tensor_scale,
                                 void *codes, void *scales, void *cuda_stream);
 
-/* codes and scales -> out device bf16 [rows, k]: element * scale (* g, NULL
- * means 1, with either format), in fp32, rounded once. */
+/* codes and scales -> out device bf16 [rows, k]: element * fl(scale * g), or
+ * (element * scale) * g where scale * g passes fp32, in fp32, rounded to bf16
+ * (g: NULL means 1, with either format). */
 h3dit_status h3dit_fp4_dequantize(h3dit_ctx *ctx, int32_t format, const void *codes,
                                   const void *scales, const float *tensor_scale, int32_t rows,
                                   int32_t k, void *out, void *cuda_stream);

@@ -177,6 +177,35 @@ def test_tiny_matrices_stay_finite(ctx, size, f32):
     assert torch.isfinite(prod).all()
 
 
+@FMTS
+def test_values_of_every_scale(ctx, fmt):
+    """All 256 scale bytes under tensor scales small, ordinary and large: values that
+    bf16 holds are those, what passes it is infinite, zeros are zeros."""
+    bs = R.BLOCK[fmt]
+    blocks = 256 if fmt == R.MX else 128                  # E4M3 scales carry no sign
+    byte = np.arange(blocks, dtype=np.uint8)[None]
+    codes = np.resize(np.arange(16, dtype=np.uint8), (1, blocks * bs))
+    q, sf = dev(R.pack(codes)), dev(R.sf_layout(byte))
+    for g in (None, 2.0 ** -149, 1e-30, 0.7, 2.0, 3.0, 4.0, 1e20, 1e36, 3e38):
+        out = torch.full((1, blocks * bs), 9.0, dtype=torch.bfloat16, device="cuda")
+        t = None if g is None else dev(np.array([g], np.float32))
+        ctx.fp4_dequantize(fmt, q, sf, out, tensor_scale=t)
+        ok(ctx)
+        g32 = np.float32(1 if g is None else g)
+        ref, got = R.values(fmt, codes, byte, g32), to_np(out)
+        assert np.array_equal(np.isnan(got), np.isnan(ref)), g
+        fin, top = ~np.isnan(ref), (2 - 2.0 ** -8) * 2.0 ** 127  # from here on bf16 rounds to infinity
+        with np.errstate(invalid="ignore"):
+            big = np.abs(ref) >= top * (1 + 2.0 ** -22)
+            # two fp32 products, either perhaps subnormal (the scale's 2^-150 grows up to six
+            # times), then bf16's own rounding, perhaps subnormal too
+            err = (2.0 ** -8 + 2.0 ** -22) * np.abs(ref) + 2.0 ** -134 + 7 * 2.0 ** -150
+            near = fin & (np.abs(ref) < top * (1 - 2.0 ** -22))
+            assert np.all(np.abs(got - ref)[near] <= err[near]), g
+        assert np.all(np.isinf(got[fin & big])), g
+        assert not got[fin & (ref == 0)].any(), g
+
+
 def test_tensor_scale_needs_nothing_of_its_scratch():
     """Whatever an earlier call, or an overlap that the rules forbid, left in the
     workspace: the scale is right, eagerly and replayed."""
