@@ -47,8 +47,9 @@ struct Kb {  // scale blocks per k-block, and MMAs that share one
   static constexpr int PER_CHUNK = 4 / CHUNKS;
 };
 
-// alpha = ga * gw, as a factor and a second one that is 1 unless the product
-// leaves the normal range of fp32.
+// alpha = ga * gw, as a factor and a second one, applied first, that is 1 unless
+// the product leaves the normal range of fp32. Then it is the larger of the two: a sum
+// times the smaller may be subnormal, and lose its bits, where the whole is not.
 struct Alpha {
   float a, b;
 };
@@ -56,7 +57,7 @@ H3_DEV Alpha tensor_alpha(const float *ga, const float *gw) {
   const float x = ga ? __ldg(ga) : 1.f, y = gw ? __ldg(gw) : 1.f;
   const float p = x * y;
   if (fabsf(p) >= 1.17549435e-38f && fabsf(p) < INFINITY) return {p, 1.f};
-  return {x, y};
+  return fabsf(x) < fabsf(y) ? Alpha{x, y} : Alpha{y, x};
 }
 
 // erf GELU of two values, x Phi(x) = max(x, 0) - |x| q with q = erfc(|x| / sqrt 2) / 2

@@ -389,6 +389,37 @@ def test_linear_many_tiles_and_tensor_scales_out_of_range(ctx, fmt):
 
 
 @FMTS
+@pytest.mark.parametrize("m", [3, 1300], ids=["few_rows", "pairs"])
+def test_tensor_scales_below_the_normal_range(ctx, fmt, m):
+    """A sum of 1.5 under 2^22 and 2^-149, either of them A's: 1.5 * 2^-127, which
+    fp32 holds; and under 2^100 and 2^30: past fp32, but not with a sum of 2^-20."""
+    from image_generation_b200 import h3dit as H
+
+    n, k = 2112, 64
+    a, w = np.zeros((m, k), np.uint8), np.zeros((n, k), np.uint8)
+    a[:, 0], w[:, 0] = 3, 2                               # 1.5 and 1
+    unit = 127 if fmt == R.MX else 0x38
+    asf, wsf = (dev(R.sf_layout(np.full((r, k // R.BLOCK[fmt]), unit, np.uint8))) for r in (m, n))
+    a, w = dev(R.pack(a)), dev(R.pack(w))
+    s = lambda v: torch.full((1,), v, device="cuda")  # noqa: E731
+    for x, y in ((2.0 ** 22, 2.0 ** -149), (2.0 ** -149, 2.0 ** 22)):
+        out = torch.zeros(m, n, device="cuda")
+        ctx.linear_fp4(fmt, H.H3DIT_EPI_GATED_RESIDUAL, a, asf, w, wsf, out, a_scale=s(x), w_scale=s(y),
+                       gate=torch.full((n,), 2.0 ** 100, device="cuda"))
+        ok(ctx)
+        assert torch.all(out == 1.5 * 2.0 ** -27), (x, y, out[0, 0].item())
+    # sums that are small by their scales: 1.5 * 2^-20 (E8M0) or 1.5 * 2^-18 (E4M3: 2^-9 each)
+    low, total = (117, -20) if fmt == R.MX else (1, -18)
+    asf, wsf = (dev(R.sf_layout(np.full((r, k // R.BLOCK[fmt]), low, np.uint8))) for r in (m, n))
+    for x, y in ((2.0 ** 100, 2.0 ** 30), (2.0 ** 30, 2.0 ** 100)):
+        out = torch.zeros(m, n, device="cuda")
+        ctx.linear_fp4(fmt, H.H3DIT_EPI_GATED_RESIDUAL, a, asf, w, wsf, out, a_scale=s(x), w_scale=s(y),
+                       gate=torch.ones(n, device="cuda"))
+        ok(ctx)
+        assert torch.all(out == 1.5 * 2.0 ** (130 + total)), (x, y, out[0, 0].item())
+
+
+@FMTS
 def test_nan_scales_reach_their_rows_only(ctx, fmt):
     from image_generation_b200 import h3dit as H
 
