@@ -1878,7 +1878,9 @@ h3dit_status h3dit_linear_fp4(h3dit_ctx *ctx, int32_t format, int32_t epilogue, 
     return ctx->fail(H3DIT_ERR_UNSUPPORTED, "FP4 linear: n = %d is not a multiple of %d", n,
                      out_sf ? 64 : 32);
   if (m == 0) return H3DIT_OK;
-  if ((static_cast<long long>(m) + 127) / 128 * ((static_cast<long long>(n) + 63) / 64) > INT_MAX)
+  // the kernels' row and column indexes run to the end of the last 256 x 256 tile
+  if (m > INT_MAX - 255 || n > INT_MAX - 255 ||
+      (static_cast<long long>(m) + 127) / 128 * ((static_cast<long long>(n) + 63) / 64) > INT_MAX)
     return ctx->fail(H3DIT_ERR_UNSUPPORTED, "FP4 linear: %d x %d is too large", m, n);
   for (const void *ptr : {a, a_sf, w, w_sf, static_cast<const void *>(out)})
     if (!ptr || !aligned16(ptr))

@@ -467,7 +467,8 @@ h3dit_status h3dit_fp4_dequantize(h3dit_ctx *ctx, int32_t format, const void *co
                                   int32_t k, void *out, void *cuda_stream);
 
 /* FP4 linear: v = (a_scale w_scale) sum_k A W + bias with A [m, k] and W [n, k]
- * FP4 matrices of one format, fp32 accumulation; k a multiple of 64, n of 32.
+ * FP4 matrices of one format, fp32 accumulation; k a multiple of 64, n of 32; m
+ * and n up to 2^31 - 256, ceil(m / 128) ceil(n / 64) below 2^31.
  * a_scale, w_scale: device fp32 scalars or NULL for 1; bias: device fp32 [n] or
  * NULL. Epilogues:
  *   STORE           out device bf16 [m, n] = v

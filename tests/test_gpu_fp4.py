@@ -621,3 +621,17 @@ def test_refusals(ctx):
     lin(a=e(0, 64), a_sf=e(0), out=b(0, 32))
     assert ctx.launch_count() == n0
     ok(ctx)
+
+
+def test_linear_refuses_what_its_indexes_cannot_reach(ctx):
+    """Row and column counts whose last tile ends past 31 bits, and too many tiles:
+    refused on the host, before any pointer is followed."""
+    from image_generation_b200 import h3dit as H
+
+    n0 = ctx.launch_count()
+    p = torch.zeros(4096, dtype=torch.uint8, device="cuda").data_ptr()
+    top = 2 ** 31 - 1
+    for m, n in ((top, 32), (top - 254, 64), (4, top - 31), (4, top // 32 * 32), (2 ** 30, 2 ** 14)):
+        assert H.lib.h3dit_linear_fp4(ctx.handle, 0, H.H3DIT_EPI_STORE, p, p, None, p, p, None, m, n, 64, p, None,
+                                      None, None, None, None, None) == H.H3DIT_ERR_UNSUPPORTED, (m, n)
+    assert ctx.launch_count() == n0
