@@ -2048,7 +2048,8 @@ h3dit_status h3dit_rope_axes(h3dit_ctx *ctx, const h3dit_rope_spec *spec, const 
     const double step = std::exp(-log_theta / (p.sec[i] ? p.sec[i] : 1));
     double w = 0.0;
     for (int j = 0; j < p.sec[i]; ++j) {
-      // every eighth anew: seven products lose less than 1e-15
+      // every eighth anew: the products between leave w good to 2.5e-15 at theta 1e4, and to
+      // 2.2e-14 anywhere in fp32 (step's rounding grows with |log theta| / s, sevenfold)
       w = j % 8 ? w * step : std::exp(-log_theta * j / p.sec[i]) / 3.14159265358979323846;
       p.half_turns[at++] = w;
     }

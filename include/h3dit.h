@@ -542,7 +542,7 @@ typedef struct h3dit_rope_spec {
  * q_out, k_out of the same type with row strides ld_q_out, ld_k_out; each output
  * may be its input with the same stride (else they must not overlap). positions:
  * device fp32 [n, 3], fractions and negative ones too; an angle is good to about
- * 1e-7 for positions up to 1e6. q_weight, k_weight: device fp32 [head_dim]: with
+ * 1e-7 for positions up to 1e6 and theta >= 1 (below, angles exceed positions). q_weight, k_weight: device fp32 [head_dim]: with
  * either not NULL both Q and K heads are RMS-normalised (norm_eps) before they
  * turn, by the weight that is given, or 1. heads_q or heads_k may be 0 (its
  * pointers are then not examined). A weight with H3DIT_ROPE_INVERSE is

@@ -121,6 +121,24 @@ def test_far_positions_and_the_table_of_the_block(ctx):
     assert (got - table).abs().max().item() <= 4e-7
 
 
+@pytest.mark.parametrize("theta", [1.0, 1e4, 2.0 ** 100, 3e38])
+def test_positions_up_to_a_million(ctx, theta):
+    """The angle's promise over the bases: its frequency is good to 2.2e-14, so at 1e6
+    it is off by 2.2e-8 beside the 9.4e-8 of its last rounding: within TURN."""
+    from image_generation_b200 import h3dit as H
+
+    n, dh, sec = 64, 256, (43, 42, 43)
+    pos = np.random.default_rng(6).uniform(-1e6, 1e6, (n, 3)).astype(np.float32)
+    q, qt = rows(n, 2 * dh, 1, True, 0)
+    for inter in (False, True):
+        out = torch.empty_like(qt)
+        ctx.rope_axes(H.make_rope_spec(dh, sec, theta, interleaved=inter), dev(pos), qt, out, 2)
+        ok(ctx)
+        t = float(np.float32(theta))
+        ref, size = R.rope(q.reshape(n, 2, dh), pos, sec, t, inter)
+        assert np.all(np.abs(to_np(out).reshape(n, 2, dh) - ref) <= bound(ref, size, True, False))
+
+
 @pytest.mark.parametrize("inter,sec", [(False, (16, 16, 16)), (True, (16, 16, 16)), (False, (5, 7, 9))])
 def test_in_place_and_inverse_is_the_gradient(ctx, inter, sec):
     from image_generation_b200 import h3dit as H
