@@ -349,6 +349,33 @@ def assert_quantized(fmt, q, sf, y, g, flips=2e-3):
 
 
 @FMTS
+@pytest.mark.parametrize("m,n,k", [(5, 192, 704), (6, 192, 6144), (140, 192, 6144), (129, 2112, 192), (1301, 2112, 704),
+                                   (1301, 2176, 704)])
+def test_scales_of_an_fp4_output(ctx, fmt, m, n, k):
+    """One part of k, several, and pairs: a row's last group of four scales is whole,
+    with zeros past the row's end, and bytes of no row are left as they were."""
+    from image_generation_b200 import h3dit as H
+
+    a, asf, av = operand(fmt, m, k, 1, True)
+    w, wsf, wv = operand(fmt, n, k, 2, True)
+    q = torch.zeros(m, n // 2, dtype=torch.uint8, device="cuda")
+    sf = torch.full((R.sf_bytes(fmt, m, n),), 0xEE, dtype=torch.uint8, device="cuda")
+    s = torch.full((1,), 0.01, device="cuda")
+    t = np.float32(0.01)
+    ctx.linear_fp4(fmt, H.H3DIT_EPI_GELU, a, asf, w, wsf, q, out_sf=sf, a_scale=s,
+                   out_scale=dev(np.array([t])) if fmt == R.NV else None)
+    ok(ctx)
+    assert_quantized(fmt, q, sf, R.gelu(float(np.float32(0.01)) * (av @ wv.T)), t)
+    blocks = n // R.BLOCK[fmt]
+    full = -(-blocks // 4) * 4
+    got, at = sf.cpu().numpy(), R.sf_index(m, full)
+    assert not got[at[:, blocks:]].any()
+    rest = np.ones(got.size, bool)
+    rest[at] = False
+    assert np.all(got[rest] == 0xEE)
+
+
+@FMTS
 @pytest.mark.parametrize("m,n,k", [(77, 256, 1024), (300, 384, 5376)])
 def test_linear_over_the_scales_range(ctx, fmt, m, n, k):
     from image_generation_b200 import h3dit as H

@@ -246,3 +246,34 @@ def test_two_contexts_on_two_streams(fmt):
     for i in range(2):
         ok(libs[i].ctx)
         assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
+
+
+@FMTS
+def test_calls_allocate_nothing(fmt):
+    """Repeated calls take nothing of the device's memory, nor of torch's."""
+    from image_generation_b200 import h3dit as H
+
+    c = make_ctx(D)
+    e = lambda *s, dt=torch.bfloat16: torch.ones(*s, dtype=dt, device="cuda")  # noqa: E731
+    x, xo, y, out = e(N, D, dt=torch.float32), e(N, D, dt=torch.float32), e(N, D), e(N, D)
+    q, sf = e(N, D // 2, dt=torch.uint8), e(R.sf_bytes(fmt, N, D), dt=torch.uint8)
+    w, wsf = e(D, D // 2, dt=torch.uint8), e(R.sf_bytes(fmt, D, D), dt=torch.uint8)
+    t, pos = e(1, dt=torch.float32), e(N, 3, dt=torch.float32)
+    kind = H.H3DIT_NORM_OUT_FP4_NV if fmt == R.NV else H.H3DIT_NORM_OUT_FP4_MX
+    ts, spec = (t if fmt == R.NV else None), H.make_rope_spec(DH, SEC)
+
+    def go():
+        c.gated_norm(x, xo, kind, q, out_sf=sf, out_scale=ts, branch=y)
+        c.linear_fp4(fmt, H.H3DIT_EPI_STORE, q, sf, w, wsf, out, a_scale=ts)
+        c.rope_axes(spec, pos, out, out, HEADS)
+        c.fp4_tensor_scale(out, t)
+        c.fp4_quantize(fmt, out, q, sf, tensor_scale=ts)
+        c.fp4_dequantize(fmt, q, sf, y, tensor_scale=ts)
+
+    go()
+    ok(c)
+    held, free = torch.cuda.memory_allocated(), torch.cuda.mem_get_info()[0]
+    for _ in range(20):
+        go()
+    ok(c)
+    assert torch.cuda.memory_allocated() == held and torch.cuda.mem_get_info()[0] >= free

@@ -158,6 +158,27 @@ def test_mxfp8_output_is_the_modulated_norms(ctxs):
     assert (q.int() - q2.int()).abs().max().item() <= 1 or (sf != sf2).any()
 
 
+def test_mxfp8_codes_block_by_block(ctxs):
+    """Beside h3dit_rmsnorm_modulate_mx, in every block under the same scale no code is
+    more than a step off and few are; blocks under another scale are a step of it off."""
+    from image_generation_b200 import h3dit as H
+
+    n, d = 300, 5376
+    ctx = ctx_for(ctxs, d)
+    i = inputs(n, d, 1, 14, False)
+    _, q, sf, _, _, _ = run(ctx, i, n, d, 1, False, False, 1, ("shift", "scale"), r=1.0)
+    q2 = torch.zeros(n * d, dtype=torch.uint8, device="cuda")
+    sf2 = torch.zeros(H.mx_scale_bytes(n, d), dtype=torch.uint8, device="cuda")
+    ctx.rmsnorm_modulate_mx(dev(i["x"]), dev(i["mod"][0, 1]), dev(i["mod"][0, 2]), q2, sf2)
+    ok(ctx)
+    at = R.sf_index(n, d // 32)
+    a, b = (s.cpu().numpy()[at].astype(int) for s in (sf, sf2))
+    assert np.abs(a - b).max() <= 1 and np.mean(a != b) <= 1e-4
+    order = lambda t: np.where(t < 128, t, 128 - t)  # noqa: E731  codes in the order of their values
+    step = np.abs(order(to_np(q).astype(int)) - order(to_np(q2).astype(int))).reshape(n, d // 32, 32)[a == b]
+    assert step.max() <= 1 and np.mean(step) <= 2e-3
+
+
 def test_zero_rows_and_nan_rows(ctxs):
     n, d = 6, 768
     ctx = ctx_for(ctxs, d)

@@ -72,6 +72,29 @@ def test_heads(ctx, dh, sec, inter, norm, f32):
         assert np.all(np.abs(to_np(o.t).reshape(n, h, dh) - ref) <= bound(ref, size, f32, norm) + 1e-30)
 
 
+@pytest.mark.parametrize("which", ["q", "k"])
+@pytest.mark.parametrize("dh,sec,inter", [(96, (16, 16, 16), False), (128, (22, 21, 21), True), (80, (5, 7, 9), False),
+                                          (112, (8, 0, 24), False), (112, (9, 0, 24), False), (240, (1, 0, 31), True)],
+                         ids=str)
+def test_one_weight_norms_both(ctx, dh, sec, inter, which):
+    """With a weight for Q or K alone both are normalised, the other by 1, also where the
+    lane in which the rotation ends reads its weights again."""
+    from image_generation_b200 import h3dit as H
+
+    n, hq, hk = 41, 5, 2
+    pos = positions(n, dh)
+    q, qt = rows(n, hq * dh, 1, True, 0)
+    k, kt = rows(n, hk * dh, 2, True, 0)
+    wt = (1 + 0.3 * np.random.default_rng(3).standard_normal(dh)).astype(np.float32)
+    qo, ko = torch.empty_like(qt), torch.empty_like(kt)
+    ctx.rope_axes(H.make_rope_spec(dh, sec, interleaved=inter), dev(pos), qt, qo, hq, kt, ko, hk,
+                  **{which + "_weight": dev(wt)})
+    ok(ctx)
+    for name, x, o, h in (("q", q, qo, hq), ("k", k, ko, hk)):
+        ref, size = R.rope(x.reshape(n, h, dh), pos, sec, 10000.0, inter, wt if name == which else None, True)
+        assert np.all(np.abs(to_np(o).reshape(n, h, dh) - ref) <= bound(ref, size, True, True) + 1e-30), name
+
+
 @pytest.mark.parametrize("n", [1, 2, 700, 5000])
 def test_token_counts(ctx, n):
     """One token to several per CTA, with a ragged end; only keys, only queries."""
