@@ -13,11 +13,13 @@
 // and its use; a scale block of the output (16 or 32 elements) spans four or
 // eight neighbouring lanes. The next rows are on their way to shared memory
 // meanwhile (cp.async, each thread its own columns, so nobody waits for
-// another's copy). 16896 x 5376 with a bf16 branch and output: 164 us, 6.6 TB/s of
-// the 1.09 GB that it cannot do without (306 with loads to registers and the
-// modulation read for every row; 260 with 32 bytes per lane instead of 16; 209 and
-// 189 with twice and one and a half times the instructions of now; two rows in hand
-// per barrier 273, out of registers).
+// another's copy). 16896 x 5376 with a bf16 branch and output: 161 us replayed on the
+// same buffers, 167 on three sets in turn, 184 called with new ones each time (5.9 TB/s
+// of the 1.09 GB that it cannot do without); MXFP8 rows 198, MXFP4 198, NVFP4 215, where a
+// chunk of 4 elements takes up to 3 shuffles and a scale. What was tried, on the same
+// buffers: 306 with loads to registers and the modulation read for every row; 260 with 32
+// bytes per lane instead of 16; 209 and 189 with twice and one and a half times the
+// instructions of now; two rows in hand per barrier 273, out of registers.
 #include "fp4.cuh"
 
 namespace h3 {

@@ -18,8 +18,11 @@
 //
 // Bound, large: by what the tensor cores and L2 give at the card's power. NVFP4
 // 8192^3 196 us (5.6 PFLOP/s; MMAs and loads alone 154, with the scales' copies 179),
-// MXFP4 16896 x 14336 x 5376 with GELU 486 us (5.4; 412 without an epilogue), NVFP4
-// 4608 x 5376 x 14336 into the residual 157. Few rows: by reading W. One row x 32256
+// MXFP4 16896 x 14336 x 5376 with GELU 486 us in a short run (5.4; 412 without an
+// epilogue), 564 in a long one at the power limit and 539 with FP4 rows, NVFP4 4608 x
+// 5376 x 14336 into the residual 157, 189 called with new operands each time (that
+// instance spills: 60 bytes stored and 224 loaded per thread and tile, with 16 warps 132
+// and 136). Few rows: by reading W. One row x 32256
 // x 5376 13.8 us with W partly in L2, 21 from HBM (97.5 MB).
 //
 // k is a multiple of 64: a last k-block with fewer than four groups of 64 reads

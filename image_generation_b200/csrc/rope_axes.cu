@@ -17,8 +17,11 @@
 // token. Positions are fp32, so the angle is formed and reduced to a half turn in
 // fp64 (far positions). The warp's next heads are on their way to shared memory
 // (cp.async, whole lines at a time).
-// 16896 tokens x 112 heads x 96: 118 us, 6.1 TB/s (181 with cosines in shared
-// memory per head, 164 with loads to registers); 20736 x 64 x 128, neighbours: 111.
+// 16896 tokens x 112 heads x 96: 118 us replayed, 129 called on new rows each time, 5.6
+// TB/s (replayed, 181 with cosines in shared memory per head, 164 with loads to
+// registers); 20736 x 64 x 128, neighbours: 112 and 123. Sections that are not multiples of
+// 8 pairs, split, are another matter: 2-byte accesses and a pair's place worked out per
+// head, 967 us where neighbours take 154 (16896 x 112 x 128).
 #include <type_traits>
 
 #include "kernels.h"
