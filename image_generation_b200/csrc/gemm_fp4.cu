@@ -21,8 +21,8 @@
 // MXFP4 16896 x 14336 x 5376 with GELU 486 us in a short run (5.4; 412 without an
 // epilogue), 564 in a long one at the power limit and 539 with FP4 rows, NVFP4 4608 x
 // 5376 x 14336 into the residual 157, 189 called with new operands each time (that
-// instance spills: 60 bytes stored and 224 loaded per thread and tile, with 16 warps 132
-// and 136). Few rows: by reading W. One row x 32256
+// instance spills, 60 bytes stored and 224 loaded by ptxas's count, with 16 warps 132 and
+// 136). Few rows: by reading W. One row x 32256
 // x 5376 13.8 us with W partly in L2, 21 from HBM (97.5 MB).
 //
 // k is a multiple of 64: a last k-block with fewer than four groups of 64 reads
